@@ -311,6 +311,142 @@ dkv_status deltakv_decode_attention_noalloc(const dkv_shape* shape, const dkv_pa
                                             int32_t max_ctx, float softmax_scale, void* out, float* lse,
                                             void* stream);
 
+/* ------------------------------------------------------------------------------------------------------------
+ * 8-bit paged cache: every token kept, K and V as 8-bit codes with one scale per block of tokens and head.
+ *
+ * No counterpart on the DeltaKV pages, which compress the long past and leave open how a serving engine holds the
+ * tokens that are not compressed (recent ones, short sequences, prompts being prefilled).  This cache holds them at
+ * half the bytes of bf16.  deltakv_kv8_append writes it, deltakv_kv8_attention attends over it, and
+ * deltakv_merge_attention joins that result with deltakv_decode_attention's over the compressed part of the same
+ * sequence, by their log-sum-exps.
+ *
+ * Layout (one dkv_kv8_cache per layer; B = block_tokens, d = head_dim):
+ *   codes   [num_blocks][H_kv][2][B][d]  8-bit codes of K (index 0) and V (index 1)
+ *   scales  [num_blocks][H_kv][2]        float32; a value is code * scale
+ * Block tables are those of the compressed cache: logical block b holds positions bB .. bB+B-1.
+ *
+ * Codes: DKV_KV8_INT8 two's complement in [-127, 127]; DKV_KV8_E4M3 OCP 8-bit floats (4 exponent bits, no
+ * infinities, largest 448).  With top = 127 or 448, the rows that one append writes into a block and half h have
+ *     s_h = max(max |x|, 2^-64) * (1 / top),     code = sat(RNE(x * (1 / s_h)))       (fp32, in this order)
+ * If the block already holds earlier rows of the sequence (the append starts inside it), s_h is at least the stored
+ * scale, and when it grows the earlier rows' codes become sat(RNE(code * (s_old * (1 / s_h)))).  A scale never
+ * shrinks while its block is filled.  A value that is not finite sets the scale to NaN and its call's codes to 0: every
+ * value of that block, head and half then reads as NaN until an append writes the block from its first row again.
+ * ------------------------------------------------------------------------------------------------------------ */
+typedef enum dkv_kv8_code { DKV_KV8_INT8 = 0, DKV_KV8_E4M3 = 1 } dkv_kv8_code;
+
+/* Supported: head_dim 64 or 128; block_tokens 16, 32 or 64; num_q_heads = G * num_kv_heads with 1 <= G <= 16;
+ * dtype (K, V, q, out) DKV_BF16 or DKV_F32. */
+typedef struct dkv_kv8_shape {
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t head_dim;
+  int32_t block_tokens;
+  int32_t dtype; /* dkv_dtype */
+  int32_t code;  /* dkv_kv8_code */
+} dkv_kv8_shape;
+
+/* Device arrays, 16-byte aligned. */
+typedef struct dkv_kv8_cache {
+  void* codes;
+  float* scales;
+  int32_t num_blocks;
+} dkv_kv8_cache;
+
+/* Position rotation.  Row p of `table` holds rot_dim / 2 cosines, then as many sines, of position p's angles.  With
+ * c = cos_i, s = sin_i, dimensions (x, y) become (x c - y s, y c + x s), each product and sum rounded to fp32; pair i
+ * is dimensions (i, i + rot_dim / 2), or (2i, 2i + 1) when `pairs` is set.  Dimensions from rot_dim on stay. */
+typedef struct dkv_kv8_rope {
+  const float* table;       /* [max_pos][rot_dim] (device, 16-byte aligned)                                  */
+  const int32_t* positions; /* [total_new] angle position of each new token (device), or NULL: its position
+                               in the sequence                                                               */
+  int32_t max_pos;          /* a position outside [0, max_pos) is recorded (DKV_DEVERR_BOUNDS), its row not
+                               rotated                                                                       */
+  int32_t rot_dim;          /* a multiple of 16, at most head_dim                                            */
+  int32_t pairs;
+} dkv_kv8_rope;
+
+/* Scores and visibility.  Query token i of a sequence with T cached tokens and n query tokens stands at position
+ * p = T - n + i.  Key t has the score
+ *     s = cap(softmax_scale q.k_t) - slope_h |p - t|,    cap(x) = softcap tanh(x / softcap)  (softcap > 0)
+ * and is seen iff  t < T,  (t <= p and (window == 0 or p - t < window)) or t < prefix_len,  and t >= first_key. */
+typedef struct dkv_kv8_score {
+  float softcap;                /* 0: none                                                                   */
+  int32_t window;               /* 0: none                                                                   */
+  const float* alibi_slopes;    /* [H_q] distance bias (device) or NULL                                      */
+  const int32_t* prefix_lens;   /* [num_seqs] keys below it are seen by every query: a bidirectional prefix, or
+                                   first tokens that stay visible beyond the window (device) or NULL         */
+  const int32_t* first_key;     /* [total_q] first visible key of each query row: the start of its document in a
+                                   packed sequence (device) or NULL                                          */
+} dkv_kv8_score;
+
+/* Sizes (bytes) of the two cache arrays for `num_blocks` blocks.  Host outputs. */
+dkv_status deltakv_kv8_cache_bytes(const dkv_kv8_shape* shape, int32_t num_blocks, size_t* codes_bytes,
+                                   size_t* scales_bytes);
+
+/*
+ * deltakv_kv8_append -- rotate, quantise and append new tokens of `num_seqs` sequences; rotate their queries.
+ *
+ *   k_new, v_new  rows of new tokens, sequences concatenated: token i, kv head h at k_new + i * k_stride + h * d
+ *                 (strides in elements, multiples of 16 bytes, at least H_kv * d; so views of a fused projection fit)
+ *   cu_new, start_pos, block_tables, total_new, max_new  as in deltakv_compress; only the blocks that hold new
+ *                 tokens need be mapped.  Two sequences of a call never write the same physical block.
+ *   rope          NULL: no rotation
+ *   q, q_out      NULL, or queries of the same tokens to be rotated by the same angles: q strided like k_new (H_q
+ *                 heads), q_out [total_new][H_q][d]; needs `rope`.  q_out may be q (same address, stride H_q * d)
+ * Writes the new tokens' codes, their blocks' scales (and re-coded earlier rows of a block whose scale grew) and
+ * q_out; all else stays as it was.
+ */
+dkv_status deltakv_kv8_append(const dkv_kv8_shape* shape, const dkv_kv8_cache* cache, const dkv_kv8_rope* rope,
+                              const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
+                              const int32_t* cu_new, const int32_t* start_pos, const int32_t* block_tables,
+                              int32_t max_blocks, int32_t num_seqs, int64_t total_new, int32_t max_new, const void* q,
+                              int64_t q_stride, void* q_out, void* stream);
+
+/* Workspace needed by deltakv_kv8_attention for these host-side bounds (host output `bytes`). */
+dkv_status deltakv_kv8_attention_workspace(const dkv_kv8_shape* shape, int32_t num_seqs, int64_t total_q,
+                                           int32_t max_q, int32_t max_ctx, size_t* bytes);
+
+/*
+ * deltakv_kv8_attention -- attention of one or many query tokens per sequence over the 8-bit cache.
+ *
+ * The query tokens of a sequence are its last ones: append first, then attend.  For query head h and the keys that
+ * its token sees (dkv_kv8_score; NULL: causal),
+ *   out = sum_t softmax_t(s_t) v_t  (rounded to dtype),   lse = log sum_t exp(s_t);   no key: out = 0, lse = -inf.
+ *
+ *   q             query row i, head h at q + i * q_stride + h * d (stride in elements, a multiple of 16 bytes)
+ *   cu_q          [num_seqs+1] int32 prefix sums of the query tokens, or NULL: one per sequence (total_q = num_seqs)
+ *   context_lens  [num_seqs] int32, 0 <= T <= max_ctx, the query tokens among them
+ *   block_tables  [num_seqs][max_blocks] int32; blocks that no query sees need not be mapped
+ *   total_q, max_q, max_ctx  host-side bounds: query rows; most query tokens of one sequence; longest context
+ *   softmax_scale <= 0 selects 1/sqrt(d)
+ *   out           [total_q][H_q][d] dtype;  lse [total_q][H_q] float32 or NULL.  Rows of no sequence stay as they were
+ *   workspace     >= deltakv_kv8_attention_workspace(shape, num_seqs, total_q, max_q, max_ctx) bytes, 256-byte
+ *                 aligned; NULL when that is 0
+ * A sequence whose lengths break a bound is recorded (DKV_DEVERR_BOUNDS) and its rows are left as they were.
+ */
+dkv_status deltakv_kv8_attention(const dkv_kv8_shape* shape, const dkv_kv8_cache* cache, const dkv_kv8_score* score,
+                                 const void* q, int64_t q_stride, const int32_t* cu_q, const int32_t* context_lens,
+                                 const int32_t* block_tables, int32_t max_blocks, int32_t num_seqs, int64_t total_q,
+                                 int32_t max_q, int32_t max_ctx, float softmax_scale, void* out, float* lse,
+                                 void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * deltakv_merge_attention -- joins attention results of the same queries over disjoint sets of keys.
+ *
+ *   lse = log sum_i exp(lse_i),   out = sum_i exp(lse_i - lse) out_i   (fp32, rounded to dtype at the end)
+ * A part with lse_i = -inf adds nothing, whatever its out_i holds; all parts so: out = 0, lse = -inf.
+ *
+ *   dtype      DKV_BF16 or DKV_F32;  head_dim 64 or 128;  num_parts 1 .. DKV_MERGE_MAX_PARTS
+ *   outs       host array of device pointers, each [num_rows][head_dim] (16-byte aligned); a row is a query and head
+ *   lses       host array of device pointers, each [num_rows] float32
+ *   out, lse   may be one of outs and one of lses (the same address); lse may be NULL
+ */
+#define DKV_MERGE_MAX_PARTS 8
+dkv_status deltakv_merge_attention(int32_t dtype, int32_t head_dim, int64_t num_rows, int32_t num_parts,
+                                   const void* const* outs, const float* const* lses, void* out, float* lse,
+                                   void* stream);
+
 /* Error word codes recorded by kernels (see deltakv_get_device_error). */
 #define DKV_DEVERR_NONE 0
 #define DKV_DEVERR_BLOCK_ID 1    /* block table entry outside [0, num_blocks)               */

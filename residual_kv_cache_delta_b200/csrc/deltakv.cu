@@ -9,6 +9,9 @@
 #include "common.cuh"
 #include "compress.cuh"
 #include "decode.cuh"
+#include "kv8_append.cuh"
+#include "kv8_attn.cuh"
+#include "kv8_merge.cuh"
 #include "layout.h"
 #include "launch.h"
 
@@ -400,6 +403,148 @@ dkv_status deltakv_decode_attention_noalloc(const dkv_shape* shape, const dkv_pa
   if ((st = noalloc_scratch(&scratch)) != DKV_OK) return st;
   return deltakv_decode_attention(shape, params, cache, q, context_lens, block_tables, max_blocks, num_seqs, max_ctx,
                                   softmax_scale, out, lse, scratch, DKV_NOALLOC_SCRATCH_BYTES, stream);
+}
+
+}  // extern "C"
+
+namespace {
+
+dkv_status check_kv8(const dkv_kv8_shape* s) {
+  if (s == nullptr) return DKV_ERR_INVALID_ARG;
+  if (s->num_q_heads <= 0 || s->num_kv_heads <= 0 || s->head_dim <= 0 || s->block_tokens <= 0)
+    return DKV_ERR_INVALID_ARG;
+  if (s->code != DKV_KV8_INT8 && s->code != DKV_KV8_E4M3) return DKV_ERR_INVALID_ARG;
+  if (s->dtype != DKV_F32 && s->dtype != DKV_BF16) return DKV_ERR_INVALID_ARG;
+  if (s->num_q_heads % s->num_kv_heads != 0) return DKV_ERR_INVALID_ARG;
+  if (s->head_dim != 64 && s->head_dim != 128) return DKV_ERR_UNSUPPORTED;
+  if (!pow2_in(s->block_tokens, 16, 64)) return DKV_ERR_UNSUPPORTED;
+  if (s->num_q_heads / s->num_kv_heads > 16) return DKV_ERR_UNSUPPORTED;
+  return DKV_OK;
+}
+
+size_t kv8_elem(const dkv_kv8_shape* s) { return s->dtype == DKV_F32 ? 4 : 2; }
+
+// Rows of `heads` heads at a stride in elements: aligned to 16 bytes and not overlapping.
+bool kv8_rows_ok(const dkv_kv8_shape* s, const void* p, int64_t stride, int heads) {
+  return aligned16(p) && stride >= static_cast<int64_t>(heads) * s->head_dim &&
+         stride <= INT64_MAX / 64 && (static_cast<uint64_t>(stride) * kv8_elem(s)) % 16 == 0;
+}
+
+dkv_status check_kv8_cache(const dkv_kv8_shape* s, const dkv_kv8_cache* c) {
+  if (c->codes == nullptr || c->scales == nullptr || c->num_blocks <= 0) return DKV_ERR_INVALID_ARG;
+  if (!aligned16(c->codes) || !aligned16(c->scales)) return DKV_ERR_INVALID_ARG;
+  // tensor maps address the cache in rows of one token, head and half
+  if (static_cast<int64_t>(c->num_blocks) * s->num_kv_heads * 2 * s->block_tokens > INT32_MAX)
+    return DKV_ERR_UNSUPPORTED;
+  return DKV_OK;
+}
+
+dkv_status check_kv8_bounds(const dkv_kv8_shape* s, int num_seqs, int64_t total_q, int max_q, int max_ctx) {
+  if (num_seqs < 0 || total_q < 0 || max_q < 0 || max_ctx < 0) return DKV_ERR_INVALID_ARG;
+  if (total_q > static_cast<int64_t>(num_seqs) * max_q) return DKV_ERR_INVALID_ARG;
+  if (total_q > INT32_MAX / s->num_q_heads || static_cast<int64_t>(max_q) * s->num_q_heads > INT32_MAX)
+    return DKV_ERR_UNSUPPORTED;
+  if (max_ctx > INT32_MAX - 1024) return DKV_ERR_UNSUPPORTED;
+  return DKV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+dkv_status deltakv_kv8_cache_bytes(const dkv_kv8_shape* s, int32_t num_blocks, size_t* codes_bytes,
+                                   size_t* scales_bytes) {
+  const dkv_status st = check_kv8(s);
+  if (st != DKV_OK) return st;
+  if (num_blocks < 0 || codes_bytes == nullptr || scales_bytes == nullptr) return DKV_ERR_INVALID_ARG;
+  const size_t cells = static_cast<size_t>(num_blocks) * s->num_kv_heads * 2;
+  *codes_bytes = cells * s->block_tokens * s->head_dim;
+  *scales_bytes = cells * 4;
+  return DKV_OK;
+}
+
+dkv_status deltakv_kv8_append(const dkv_kv8_shape* shape, const dkv_kv8_cache* cache, const dkv_kv8_rope* rope,
+                              const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
+                              const int32_t* cu_new, const int32_t* start_pos, const int32_t* block_tables,
+                              int32_t max_blocks, int32_t num_seqs, int64_t total_new, int32_t max_new, const void* q,
+                              int64_t q_stride, void* q_out, void* stream) {
+  dkv_status st = check_kv8(shape);
+  if (st != DKV_OK) return st;
+  if (cache == nullptr || num_seqs < 0 || total_new < 0 || max_new < 0 || max_blocks < 0) return DKV_ERR_INVALID_ARG;
+  if (rope != nullptr && (rope->rot_dim <= 0 || rope->rot_dim % 16 != 0 || rope->rot_dim > shape->head_dim ||
+                          rope->max_pos <= 0 || rope->table == nullptr || !aligned16(rope->table)))
+    return DKV_ERR_INVALID_ARG;
+  if ((q == nullptr) != (q_out == nullptr) || (q != nullptr && rope == nullptr)) return DKV_ERR_INVALID_ARG;
+  if (num_seqs == 0 || total_new == 0 || max_new == 0) return DKV_OK;
+  if (total_new > static_cast<int64_t>(num_seqs) * max_new) return DKV_ERR_INVALID_ARG;
+  if (total_new > INT32_MAX) return DKV_ERR_UNSUPPORTED;
+  if (k_new == nullptr || v_new == nullptr || cu_new == nullptr || start_pos == nullptr || block_tables == nullptr)
+    return DKV_ERR_INVALID_ARG;
+  if (!kv8_rows_ok(shape, k_new, k_stride, shape->num_kv_heads) ||
+      !kv8_rows_ok(shape, v_new, v_stride, shape->num_kv_heads))
+    return DKV_ERR_INVALID_ARG;
+  if (q != nullptr && (!kv8_rows_ok(shape, q, q_stride, shape->num_q_heads) || !aligned16(q_out)))
+    return DKV_ERR_INVALID_ARG;
+  if (q != nullptr && q == q_out && q_stride != static_cast<int64_t>(shape->num_q_heads) * shape->head_dim)
+    return DKV_ERR_INVALID_ARG;
+  if ((st = check_kv8_cache(shape, cache)) != DKV_OK) return st;
+  dkv::Kv8AppendArgs a{shape,  cache,        rope,       k_new,    v_new,     k_stride, v_stride, cu_new,
+                       start_pos, block_tables, max_blocks, num_seqs, total_new, max_new,  q,        q_stride, q_out};
+  return dkv::launch_kv8_append(a, static_cast<cudaStream_t>(stream));
+}
+
+dkv_status deltakv_kv8_attention_workspace(const dkv_kv8_shape* s, int32_t num_seqs, int64_t total_q, int32_t max_q,
+                                           int32_t max_ctx, size_t* bytes) {
+  dkv_status st = check_kv8(s);
+  if (st != DKV_OK) return st;
+  if (bytes == nullptr) return DKV_ERR_INVALID_ARG;
+  if ((st = check_kv8_bounds(s, num_seqs, total_q, max_q, max_ctx)) != DKV_OK) return st;
+  *bytes = dkv::kv8_attn_layout(*s, dkv::kv8_attn_splits(*s, num_seqs, total_q, max_q, max_ctx), total_q).total;
+  return DKV_OK;
+}
+
+dkv_status deltakv_kv8_attention(const dkv_kv8_shape* shape, const dkv_kv8_cache* cache, const dkv_kv8_score* score,
+                                 const void* q, int64_t q_stride, const int32_t* cu_q, const int32_t* context_lens,
+                                 const int32_t* block_tables, int32_t max_blocks, int32_t num_seqs, int64_t total_q,
+                                 int32_t max_q, int32_t max_ctx, float softmax_scale, void* out, float* lse,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+  dkv_status st = check_kv8(shape);
+  if (st != DKV_OK) return st;
+  if (cache == nullptr || max_blocks < 0) return DKV_ERR_INVALID_ARG;
+  if (score != nullptr && (!(score->softcap >= 0.0f) || score->softcap > 3.402823466e38f || score->window < 0))
+    return DKV_ERR_INVALID_ARG;
+  if (softmax_scale != softmax_scale) return DKV_ERR_INVALID_ARG;
+  if ((st = check_kv8_bounds(shape, num_seqs, total_q, max_q, max_ctx)) != DKV_OK) return st;
+  if (cu_q == nullptr && total_q != num_seqs) return DKV_ERR_INVALID_ARG;
+  if (num_seqs == 0 || total_q == 0) return DKV_OK;
+  if (static_cast<int64_t>(max_blocks) * shape->block_tokens < max_ctx) return DKV_ERR_INVALID_ARG;
+  if (q == nullptr || context_lens == nullptr || block_tables == nullptr || out == nullptr) return DKV_ERR_INVALID_ARG;
+  if (!kv8_rows_ok(shape, q, q_stride, shape->num_q_heads) || !aligned16(out)) return DKV_ERR_INVALID_ARG;
+  if ((st = check_kv8_cache(shape, cache)) != DKV_OK) return st;
+  const dkv::Kv8AttnWs w =
+      dkv::kv8_attn_layout(*shape, dkv::kv8_attn_splits(*shape, num_seqs, total_q, max_q, max_ctx), total_q);
+  if (w.total > 0) {
+    if (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return DKV_ERR_INVALID_ARG;
+    if (workspace_bytes < w.total) return DKV_ERR_WORKSPACE;
+  }
+  dkv::Kv8AttnArgs a{shape,    cache,   score, q,       q_stride,      cu_q, context_lens, block_tables, max_blocks,
+                     num_seqs, total_q, max_q, max_ctx, softmax_scale, out,  lse};
+  return dkv::launch_kv8_attention(a, w, workspace, static_cast<cudaStream_t>(stream));
+}
+
+dkv_status deltakv_merge_attention(int32_t dtype, int32_t head_dim, int64_t num_rows, int32_t num_parts,
+                                   const void* const* outs, const float* const* lses, void* out, float* lse,
+                                   void* stream) {
+  if (dtype != DKV_F32 && dtype != DKV_BF16) return DKV_ERR_INVALID_ARG;
+  if (head_dim <= 0 || num_rows < 0 || num_parts < 1 || num_parts > DKV_MERGE_MAX_PARTS) return DKV_ERR_INVALID_ARG;
+  if (head_dim != 64 && head_dim != 128) return DKV_ERR_UNSUPPORTED;
+  if (num_rows == 0) return DKV_OK;
+  if (num_rows > INT64_MAX / 1024) return DKV_ERR_UNSUPPORTED;
+  if (outs == nullptr || lses == nullptr || out == nullptr || !aligned16(out)) return DKV_ERR_INVALID_ARG;
+  for (int i = 0; i < num_parts; ++i)
+    if (outs[i] == nullptr || lses[i] == nullptr || !aligned16(outs[i])) return DKV_ERR_INVALID_ARG;
+  return dkv::launch_merge(dtype, num_rows, head_dim, num_parts, outs, lses, out, lse,
+                           static_cast<cudaStream_t>(stream));
 }
 
 dkv_status deltakv_selftest_wait_timeout(uint64_t limit_ns, uint64_t* result, void* stream) {

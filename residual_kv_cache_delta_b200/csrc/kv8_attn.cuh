@@ -1,0 +1,59 @@
+// Launch of attention over the 8-bit cache: the split plan and the choice of kernel.
+#pragma once
+
+#include "kv8_attn_simple.cuh"
+#include "launch.h"
+
+namespace dkv {
+
+int kv8_attn_splits(const dkv_kv8_shape& sh, int num_seqs, int64_t total_q, int max_q, int max_ctx) {
+  const int64_t tiles =
+      ceil_div64(static_cast<int64_t>(max_q) * (sh.num_q_heads / sh.num_kv_heads), kSimpleRows) * sh.num_kv_heads *
+      std::max(num_seqs, 1);
+  const int64_t want = ceil_div64(int64_t{8} * num_sms(), std::max<int64_t>(tiles, 1));
+  const int64_t most = ceil_div64(max_ctx, kKv8CellKeys * kKv8MinSplitCells);
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, most, int64_t{kKv8MaxSplits}})));
+}
+
+template <typename T, int D, bool E4M3>
+static dkv_status attn_simple(const Kv8Attn& p, cudaStream_t st) {
+  const int row_tiles = static_cast<int>(ceil_div64(static_cast<int64_t>(p.max_q) * p.group, kSimpleRows));
+  const int64_t ctas = static_cast<int64_t>(p.nsplit) * row_tiles * p.heads * p.num_seqs;
+  if (ctas > INT32_MAX) return DKV_ERR_UNSUPPORTED;
+  kv8_attn_simple_kernel<T, D, E4M3><<<static_cast<unsigned>(ctas), 128, 0, st>>>(p, row_tiles);
+  if (cudaGetLastError() != cudaSuccess) return DKV_ERR_CUDA;
+  if (p.nsplit > 1) {
+    const int64_t rows = p.total_q * p.heads * p.group;
+    kv8_combine_kernel<T, D><<<static_cast<unsigned>(ceil_div64(rows, 512 / D)), 128, 0, st>>>(p);
+  }
+  return cudaGetLastError() == cudaSuccess ? DKV_OK : DKV_ERR_CUDA;
+}
+
+dkv_status launch_kv8_attention(const Kv8AttnArgs& a, const Kv8AttnWs& w, void* workspace, cudaStream_t st) {
+  const dkv_kv8_shape& sh = *a.shape;
+  Kv8Attn p = {};
+  p.codes = static_cast<const uint8_t*>(a.cache->codes);
+  p.scales = a.cache->scales;
+  p.num_blocks = a.cache->num_blocks;
+  p.heads = sh.num_kv_heads, p.group = sh.num_q_heads / sh.num_kv_heads, p.block = sh.block_tokens;
+  p.q = a.q, p.q_stride = a.q_stride, p.cu_q = a.cu_q, p.context_lens = a.context_lens;
+  p.block_tables = a.block_tables, p.max_blocks = a.max_blocks, p.num_seqs = a.num_seqs;
+  p.total_q = a.total_q, p.max_q = a.max_q, p.max_ctx = a.max_ctx;
+  p.scale = a.softmax_scale > 0.f ? a.softmax_scale : 1.0f / sqrtf(static_cast<float>(sh.head_dim));
+  if (a.score) {
+    p.softcap = a.score->softcap, p.window = a.score->window, p.slopes = a.score->alibi_slopes;
+    p.prefix_lens = a.score->prefix_lens, p.first_key = a.score->first_key;
+  }
+  p.out = a.out, p.lse = a.lse, p.nsplit = w.nsplit;
+  p.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + w.ml);
+  p.o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.o);
+  const bool e4 = sh.code == DKV_KV8_E4M3, d64 = sh.head_dim == 64;
+  if (sh.dtype == DKV_F32) {
+    if (d64) return e4 ? attn_simple<float, 64, true>(p, st) : attn_simple<float, 64, false>(p, st);
+    return e4 ? attn_simple<float, 128, true>(p, st) : attn_simple<float, 128, false>(p, st);
+  }
+  if (d64) return e4 ? attn_simple<__nv_bfloat16, 64, true>(p, st) : attn_simple<__nv_bfloat16, 64, false>(p, st);
+  return e4 ? attn_simple<__nv_bfloat16, 128, true>(p, st) : attn_simple<__nv_bfloat16, 128, false>(p, st);
+}
+
+}  // namespace dkv

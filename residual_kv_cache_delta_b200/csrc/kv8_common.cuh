@@ -1,0 +1,184 @@
+// Device-side helpers of the 8-bit paged cache: the cell layout, visibility of keys and the split of a query
+// row's keys into cells.
+//
+// A physical block holds, per kv head, `block` rows of head_dim 8-bit K codes and then as many V codes, and two
+// fp32 scales (K, V): a value is code * scale.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "kv8.h"
+
+namespace dkv {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// The running maximum of a row that has seen no key: finite, so that exp2(-inf - m) is 0 and not NaN.
+constexpr float kNoMax = -1e30f;
+
+struct Kv8Attn {
+  const uint8_t* codes;
+  const float* scales;
+  int num_blocks, heads, group, block;
+  const void* q;
+  int64_t q_stride;
+  const int* cu_q;
+  const int* context_lens;
+  const int* block_tables;
+  int max_blocks, num_seqs;
+  int64_t total_q;
+  int max_q, max_ctx;
+  float scale;    // softmax scale
+  float softcap;  // 0: none
+  const float* slopes;
+  int window;  // 0: none
+  const int* prefix_lens;
+  const int* first_key;
+  void* out;
+  float* lse;
+  int nsplit;
+  float2* ml;  // [nsplit][total_q][H_q] (maximum, sum), log2 domain
+  float* o;    // [nsplit][total_q][H_q][d]
+};
+
+// One sequence of an attention call.  ok = false: no queries, or a device length breaks its host bound (recorded);
+// its rows are left as they were.
+struct Kv8Seq {
+  int q0, nq, T, prefix;
+  bool ok;
+};
+
+__device__ __forceinline__ Kv8Seq kv8_seq(const Kv8Attn& a, int s) {
+  Kv8Seq v;
+  v.q0 = a.cu_q ? a.cu_q[s] : s;
+  v.nq = a.cu_q ? a.cu_q[s + 1] - v.q0 : 1;
+  v.T = a.context_lens[s];
+  v.prefix = a.prefix_lens ? min(max(a.prefix_lens[s], 0), v.T) : 0;
+  const bool fits = v.q0 >= 0 && v.nq >= 0 && v.nq <= a.max_q && static_cast<int64_t>(v.q0) + v.nq <= a.total_q &&
+                    v.T >= 0 && v.T <= a.max_ctx;
+  if (!fits) record_error(DKV_DEVERR_BOUNDS);
+  v.ok = fits && v.nq > 0;
+  return v;
+}
+
+// Keys that query token i of a sequence sees: [lo, hi] and [first, prefix).
+struct Kv8Row {
+  int pos, lo, hi, first;
+};
+
+__device__ __forceinline__ Kv8Row kv8_row(const Kv8Attn& a, const Kv8Seq& s, int i) {
+  Kv8Row r;
+  r.pos = s.T - s.nq + i;
+  r.first = a.first_key ? max(a.first_key[s.q0 + i], 0) : 0;
+  r.lo = a.window > 0 ? max(r.first, r.pos - a.window + 1) : r.first;
+  r.hi = r.pos;
+  return r;
+}
+
+__device__ __forceinline__ bool kv8_sees(const Kv8Row& r, int prefix, int key) {
+  return (key >= r.lo && key <= r.hi) || (key >= r.first && key < prefix);
+}
+
+// The cells (of `keys` keys each) that hold every key seen by query tokens i0 .. i1-1: [a0, a1) and [b0, b1).
+struct Kv8Span {
+  int a0, a1, b0, b1;
+  __device__ __forceinline__ int count() const { return (a1 - a0) + (b1 - b0); }
+  __device__ __forceinline__ int cell(int v) const { return v < a1 - a0 ? a0 + v : b0 + v - (a1 - a0); }
+};
+
+__device__ __forceinline__ Kv8Span kv8_span(const Kv8Seq& s, int window, int p0, int p1, int first, int keys) {
+  Kv8Span v;
+  int lo = window > 0 ? max(0, p0 - window + 1) : 0;
+  lo = max(lo, first);
+  const int hi = min(p1 + 1, s.T);
+  v.a0 = v.a1 = 0;
+  if (first < s.prefix) {
+    v.a0 = first / keys;
+    v.a1 = (s.prefix + keys - 1) / keys;
+  }
+  v.b0 = lo / keys;
+  v.b1 = hi > lo ? (hi + keys - 1) / keys : v.b0;
+  if (v.a1 > v.a0) v.b0 = max(v.b0, v.a1);
+  v.b1 = max(v.b1, v.b0);
+  return v;
+}
+
+// Cells [v0, v1) of split `split`: an even share of the span, at least kKv8MinSplitCells.
+__device__ __forceinline__ void kv8_split(int cells, int nsplit, int split, int& v0, int& v1) {
+  const int per = max((cells + nsplit - 1) / nsplit, nsplit > 1 ? kKv8MinSplitCells : 1);
+  v0 = static_cast<int>(min(static_cast<int64_t>(cells), static_cast<int64_t>(split) * per));
+  v1 = min(cells, v0 + per);
+}
+
+// Physical block of logical block b of sequence s, or -1 (recorded) when the table's entry is out of range.
+__device__ __forceinline__ int kv8_block(const int* tables, int max_blocks, int num_blocks, int s, int b) {
+  int id = -1;
+  if (b >= 0 && b < max_blocks) id = tables[static_cast<int64_t>(s) * max_blocks + b];
+  if (id < 0 || id >= num_blocks) {
+    record_error(DKV_DEVERR_BLOCK_ID);
+    return -1;
+  }
+  return id;
+}
+
+template <bool E4M3>
+__device__ __forceinline__ float kv8_decode(uint8_t c) {
+  if (E4M3) {
+    __nv_fp8_e4m3 x;
+    x.__x = c;
+    return static_cast<float>(x);
+  }
+  return static_cast<float>(static_cast<int8_t>(c));
+}
+
+// Score in the log2 domain.  dot: q.k of the dequantised key times the softmax scale (natural units).  With a cap,
+// cap * tanh(dot / cap) = cap - 2 cap / (1 + exp(2 dot / cap)): the hardware exp2 and a division keep the absolute
+// error near 1e-7 cap, where tanh.approx would leave 5e-4 cap.
+__device__ __forceinline__ float kv8_cap(float dot, float cap) {
+  const float e = exp2f(dot * (2.0f * kLog2e / cap));
+  return cap - 2.0f * cap / (1.0f + e);
+}
+
+// Merges the splits of one query row and head: out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.  Thread per
+// 4 output values.  T: out type.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) kv8_combine_kernel(const Kv8Attn a) {
+  constexpr int kVec = D / 4, kRows = 128 / kVec;
+  griddep_wait();
+  const int hq = a.heads * a.group;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kVec;
+  const int64_t rows = a.total_q * hq;
+  if (row >= rows) return;
+  if (a.cu_q) {  // rows outside every sequence stay as they were
+    const int64_t tok = row / hq;
+    int lo = 0, hi = a.num_seqs;  // the last sequence that begins at or before tok
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (a.cu_q[mid] <= tok) lo = mid; else hi = mid;
+    }
+    if (tok < a.cu_q[lo] || tok >= a.cu_q[lo + 1] || !kv8_seq(a, lo).ok) return;
+  } else if (!kv8_seq(a, static_cast<int>(row / hq)).ok) {
+    return;
+  }
+  const int c = (threadIdx.x % kVec) * 4;
+  float M = kNoMax;
+  for (int i = 0; i < a.nsplit; ++i) M = fmaxf(M, a.ml[i * rows + row].x);
+  float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int i = 0; i < a.nsplit; ++i) {
+    const float2 p = a.ml[i * rows + row];
+    if (p.y == 0.f) continue;  // nothing seen there (a NaN sum goes on)
+    const float w = exp2f(p.x - M);
+    const float4 o = *reinterpret_cast<const float4*>(a.o + (i * rows + row) * D + c);
+    l += w * p.y;
+    acc[0] += w * o.x, acc[1] += w * o.y, acc[2] += w * o.z, acc[3] += w * o.w;
+  }
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+  T* out = static_cast<T*>(a.out) + row * D + c;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) out[j] = Elem<T>::from_f(acc[j] * inv);
+  if (c == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+}
+
+}  // namespace dkv

@@ -28,7 +28,11 @@ EXPORTED = ("deltakv_status_string", "deltakv_check_shape", "deltakv_block_bytes
             "deltakv_decode_attention", "deltakv_profile_kernel", "deltakv_profile_count",
             "deltakv_get_device_error", "deltakv_decode_attention_noalloc", "deltakv_decode_sparse_workspace",
             "deltakv_decode_attention_sparse", "deltakv_compress_topk", "deltakv_decode_topk_workspace",
-            "deltakv_decode_attention_topk", "deltakv_selftest_wait_timeout")
+            "deltakv_decode_attention_topk", "deltakv_selftest_wait_timeout", "deltakv_kv8_cache_bytes",
+            "deltakv_kv8_append", "deltakv_kv8_attention_workspace", "deltakv_kv8_attention",
+            "deltakv_merge_attention")
+KV8_CODES = {"int8": 0, "e4m3": 1}
+MERGE_MAX_PARTS = 8
 NOALLOC_SCRATCH_BYTES = 16 * 1024 * 1024
 KERNEL_CENTER, KERNEL_REFPREP, KERNEL_SEARCH, KERNEL_DECODE_PROLOGUE, KERNEL_DECODE_SPLIT, KERNEL_DECODE_COMBINE = range(6)
 
@@ -45,6 +49,25 @@ class DkvParams(ctypes.Structure):
 class DkvCache(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("ref_idx", ctypes.c_void_p), ("refs", ctypes.c_void_p),
                 ("num_blocks", ctypes.c_int32)]
+
+
+class DkvKv8Shape(ctypes.Structure):
+    _fields_ = [("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("block_tokens", ctypes.c_int32), ("dtype", ctypes.c_int32), ("code", ctypes.c_int32)]
+
+
+class DkvKv8Cache(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("num_blocks", ctypes.c_int32)]
+
+
+class DkvKv8Rope(ctypes.Structure):
+    _fields_ = [("table", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("max_pos", ctypes.c_int32),
+                ("rot_dim", ctypes.c_int32), ("pairs", ctypes.c_int32)]
+
+
+class DkvKv8Score(ctypes.Structure):
+    _fields_ = [("softcap", ctypes.c_float), ("window", ctypes.c_int32), ("alibi_slopes", ctypes.c_void_p),
+                ("prefix_lens", ctypes.c_void_p), ("first_key", ctypes.c_void_p)]
 
 
 _lib = None
@@ -101,6 +124,19 @@ def load_library() -> ctypes.CDLL:
     lib.deltakv_get_device_error.restype = ctypes.c_int
     lib.deltakv_selftest_wait_timeout.argtypes = [ctypes.c_uint64, P, P]
     lib.deltakv_selftest_wait_timeout.restype = ctypes.c_int
+    pkshape, pkcache = ctypes.POINTER(DkvKv8Shape), ctypes.POINTER(DkvKv8Cache)
+    lib.deltakv_kv8_cache_bytes.argtypes = [pkshape, I32, ctypes.POINTER(SZ), ctypes.POINTER(SZ)]
+    lib.deltakv_kv8_cache_bytes.restype = ctypes.c_int
+    lib.deltakv_kv8_append.argtypes = [pkshape, pkcache, ctypes.POINTER(DkvKv8Rope), P, I64, P, I64, P, P, P, I32, I32,
+                                       I64, I32, P, I64, P, P]
+    lib.deltakv_kv8_append.restype = ctypes.c_int
+    lib.deltakv_kv8_attention_workspace.argtypes = [pkshape, I32, I64, I32, I32, ctypes.POINTER(SZ)]
+    lib.deltakv_kv8_attention_workspace.restype = ctypes.c_int
+    lib.deltakv_kv8_attention.argtypes = [pkshape, pkcache, ctypes.POINTER(DkvKv8Score), P, I64, P, P, P, I32, I32, I64,
+                                          I32, I32, ctypes.c_float, P, P, P, SZ, P]
+    lib.deltakv_kv8_attention.restype = ctypes.c_int
+    lib.deltakv_merge_attention.argtypes = [I32, I32, I64, I32, ctypes.POINTER(P), ctypes.POINTER(P), P, P, P]
+    lib.deltakv_merge_attention.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -356,6 +392,190 @@ def deltakv_decode_attention_topk(shape: Shape, k: int, mu: torch.Tensor, basis:
         _ptr(lse, torch.float32, "lse"), _ptr(workspace, torch.uint8, "workspace"), workspace.numel(),
         _stream(stream))
     _check(st, "deltakv_decode_attention_topk")
+
+
+@dataclass(frozen=True)
+class KV8Shape:
+    """Head geometry of one layer of the 8-bit cache (mirrors ``dkv_kv8_shape``); code "int8" or "e4m3"."""
+
+    num_q_heads: int
+    num_kv_heads: int
+    head_dim: int
+    block_tokens: int
+    dtype: torch.dtype = torch.bfloat16
+    code: str = "int8"
+
+    @property
+    def c(self) -> DkvKv8Shape:
+        if self.dtype not in (torch.bfloat16, torch.float32) or self.code not in KV8_CODES:
+            raise ValueError(f"KV8Shape: dtype {self.dtype}, code {self.code!r}")
+        return DkvKv8Shape(self.num_q_heads, self.num_kv_heads, self.head_dim, self.block_tokens,
+                           DKV_F32 if self.dtype == torch.float32 else DKV_BF16, KV8_CODES[self.code])
+
+    @property
+    def code_dtype(self) -> torch.dtype:
+        return torch.int8 if self.code == "int8" else torch.float8_e4m3fn
+
+
+@dataclass
+class KV8Cache:
+    """Caller-owned device arrays of one layer's 8-bit cache."""
+
+    codes: torch.Tensor   # [num_blocks, H_kv, 2, B, d] int8 or float8_e4m3fn
+    scales: torch.Tensor  # [num_blocks, H_kv, 2] float32
+
+    @property
+    def num_blocks(self) -> int:
+        return self.codes.shape[0]
+
+    def nbytes(self) -> int:
+        return sum(t.numel() * t.element_size() for t in (self.codes, self.scales))
+
+
+def alloc_kv8_cache(shape: KV8Shape, num_blocks: int, device="cuda") -> KV8Cache:
+    """Zeroed cache arrays (append writes a block before anything reads it, so their contents do not matter)."""
+    H, B, d = shape.num_kv_heads, shape.block_tokens, shape.head_dim
+    return KV8Cache(torch.zeros((num_blocks, H, 2, B, d), dtype=torch.uint8, device=device).view(shape.code_dtype),
+                    torch.zeros((num_blocks, H, 2), dtype=torch.float32, device=device))
+
+
+def kv8_cache_bytes(shape: KV8Shape, num_blocks: int) -> tuple[int, int]:
+    a, b = ctypes.c_size_t(), ctypes.c_size_t()
+    _check(load_library().deltakv_kv8_cache_bytes(ctypes.byref(shape.c), num_blocks, ctypes.byref(a), ctypes.byref(b)),
+           "deltakv_kv8_cache_bytes")
+    return a.value, b.value
+
+
+def kv8_attention_workspace(shape: KV8Shape, num_seqs: int, total_q: int, max_q: int, max_ctx: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().deltakv_kv8_attention_workspace(ctypes.byref(shape.c), num_seqs, total_q, max_q, max_ctx,
+                                                          ctypes.byref(n)), "deltakv_kv8_attention_workspace")
+    return n.value
+
+
+def _sized(t: torch.Tensor, dims: tuple, dtype: torch.dtype, name: str, dev: torch.device) -> int:
+    """Pointer of a contiguous tensor of exactly these dimensions on ``dev``."""
+    if tuple(t.shape) != tuple(dims):
+        raise ValueError(f"{name} must have shape {tuple(dims)}, got {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    return _ptr(t, dtype, name)
+
+
+def _rows(t: torch.Tensor, n: int, heads: int, shape: KV8Shape, name: str, dev: torch.device) -> tuple[int, int]:
+    """Pointer and row stride of [n, heads, d] whose rows may lie apart (a view of a fused projection)."""
+    if tuple(t.shape) != (n, heads, shape.head_dim):
+        raise ValueError(f"{name} must have shape {(n, heads, shape.head_dim)}, got {tuple(t.shape)}")
+    if t.device != dev or not t.is_cuda:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    if t.dtype != shape.dtype:
+        raise ValueError(f"{name} must be {shape.dtype}, got {t.dtype}")
+    if n > 0 and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != shape.head_dim)):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return t.data_ptr(), (t.stride(0) if n > 1 else heads * shape.head_dim)
+
+
+def _kv8_cache(shape: KV8Shape, cache: KV8Cache) -> DkvKv8Cache:
+    nb, H, B, d = cache.num_blocks, shape.num_kv_heads, shape.block_tokens, shape.head_dim
+    dev = cache.codes.device
+    return DkvKv8Cache(_sized(cache.codes, (nb, H, 2, B, d), shape.code_dtype, "cache.codes", dev),
+                       _sized(cache.scales, (nb, H, 2), torch.float32, "cache.scales", dev), nb)
+
+
+def _stream_on(stream, dev: torch.device) -> int:
+    return torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
+
+
+def deltakv_kv8_append(shape: KV8Shape, cache: KV8Cache, k_new: torch.Tensor, v_new: torch.Tensor,
+                       cu_new: torch.Tensor, start_pos: torch.Tensor, block_tables: torch.Tensor, max_new: int,
+                       rope: Optional[torch.Tensor] = None, rope_pairs: bool = False,
+                       positions: Optional[torch.Tensor] = None, q: Optional[torch.Tensor] = None,
+                       q_out: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Enqueue ``deltakv_kv8_append``.  k_new/v_new [total_new, H_kv, d] (rows may be strided); cu_new [num_seqs+1],
+    start_pos [num_seqs], block_tables [num_seqs, max_blocks] int32; rope [max_pos, rot_dim] fp32 (cosines, then
+    sines); positions [total_new] int32 or None; q [total_new, H_q, d] with q_out of the same shape, or None."""
+    dev, n = cache.codes.device, k_new.shape[0]
+    cs, cc = shape.c, _kv8_cache(shape, cache)
+    num_seqs, max_blocks = block_tables.shape
+    kp, ks = _rows(k_new, n, shape.num_kv_heads, shape, "k_new", dev)
+    vp, vs = _rows(v_new, n, shape.num_kv_heads, shape, "v_new", dev)
+    qp, qs, qo, cr = 0, 0, 0, None
+    if rope is not None:
+        cr = DkvKv8Rope(_sized(rope, rope.shape, torch.float32, "rope", dev),
+                        _sized(positions, (n,), torch.int32, "positions", dev) if positions is not None else 0,
+                        rope.shape[0], rope.shape[1], int(rope_pairs))
+    elif positions is not None:
+        raise ValueError("positions without rope")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    if q is not None:
+        qp, qs = _rows(q, n, shape.num_q_heads, shape, "q", dev)
+        qo = _sized(q_out, (n, shape.num_q_heads, shape.head_dim), shape.dtype, "q_out", dev)
+    with torch.cuda.device(dev):
+        st = load_library().deltakv_kv8_append(
+            ctypes.byref(cs), ctypes.byref(cc), ctypes.byref(cr) if cr is not None else None, kp, ks, vp, vs,
+            _sized(cu_new, (num_seqs + 1,), torch.int32, "cu_new", dev),
+            _sized(start_pos, (num_seqs,), torch.int32, "start_pos", dev),
+            _sized(block_tables, block_tables.shape, torch.int32, "block_tables", dev), max_blocks, num_seqs, n, max_new,
+            qp, qs, qo, _stream_on(stream, dev))
+    _check(st, "deltakv_kv8_append")
+
+
+def deltakv_kv8_attention(shape: KV8Shape, cache: KV8Cache, q: torch.Tensor, cu_q: Optional[torch.Tensor],
+                          context_lens: torch.Tensor, block_tables: torch.Tensor, max_q: int, max_ctx: int,
+                          out: torch.Tensor, lse: Optional[torch.Tensor], workspace: Optional[torch.Tensor],
+                          softmax_scale: float = 0.0, softcap: float = 0.0, window: int = 0,
+                          alibi_slopes: Optional[torch.Tensor] = None, prefix_lens: Optional[torch.Tensor] = None,
+                          first_key: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Enqueue ``deltakv_kv8_attention``.  q [total_q, H_q, d] (rows may be strided), out the same shape, lse [total_q,
+    H_q] fp32 or None; cu_q [num_seqs+1] or None (one query token per sequence), context_lens [num_seqs], block_tables
+    [num_seqs, max_blocks] int32; alibi_slopes [H_q] fp32, prefix_lens [num_seqs] and first_key [total_q] int32."""
+    dev, n = cache.codes.device, q.shape[0]
+    cs, cc = shape.c, _kv8_cache(shape, cache)
+    num_seqs, max_blocks = block_tables.shape
+    qp, qs = _rows(q, n, shape.num_q_heads, shape, "q", dev)
+
+    def opt(t, dims, dtype, name):
+        return 0 if t is None else _sized(t, dims, dtype, name, dev)
+
+    score = DkvKv8Score(float(softcap), int(window),
+                        opt(alibi_slopes, (shape.num_q_heads,), torch.float32, "alibi_slopes"),
+                        opt(prefix_lens, (num_seqs,), torch.int32, "prefix_lens"),
+                        opt(first_key, (n,), torch.int32, "first_key"))
+    ws = opt(workspace, (workspace.numel(),) if workspace is not None else (), torch.uint8, "workspace")
+    with torch.cuda.device(dev):
+        st = load_library().deltakv_kv8_attention(
+            ctypes.byref(cs), ctypes.byref(cc), ctypes.byref(score), qp, qs,
+            opt(cu_q, (num_seqs + 1,), torch.int32, "cu_q"),
+            _sized(context_lens, (num_seqs,), torch.int32, "context_lens", dev),
+            _sized(block_tables, block_tables.shape, torch.int32, "block_tables", dev), max_blocks, num_seqs, n, max_q,
+            max_ctx, float(softmax_scale),
+            _sized(out, (n, shape.num_q_heads, shape.head_dim), shape.dtype, "out", dev),
+            opt(lse, (n, shape.num_q_heads), torch.float32, "lse"), ws,
+            workspace.numel() if workspace is not None else 0, _stream_on(stream, dev))
+    _check(st, "deltakv_kv8_attention")
+
+
+def deltakv_merge_attention(outs, lses, out: torch.Tensor, lse: Optional[torch.Tensor], stream=None) -> None:
+    """Enqueue ``deltakv_merge_attention``: outs, lses are lists of [..., d] and [...] (fp32) tensors, the results of
+    the same queries over disjoint keys (deltakv_decode_attention*, deltakv_kv8_attention); out/lse of the same shapes."""
+    if len(outs) != len(lses) or not 1 <= len(outs) <= MERGE_MAX_PARTS:
+        raise ValueError(f"1 to {MERGE_MAX_PARTS} parts, as many lses as outs: got {len(outs)} and {len(lses)}")
+    dev, dims, dt = out.device, tuple(out.shape), out.dtype
+    if dt not in (torch.bfloat16, torch.float32) or len(dims) < 1:
+        raise ValueError(f"out: {dt} of shape {dims}")
+    n = len(outs)
+    po = (ctypes.c_void_p * n)(*[_sized(t, dims, dt, f"outs[{i}]", dev) for i, t in enumerate(outs)])
+    pl = (ctypes.c_void_p * n)(*[_sized(t, dims[:-1], torch.float32, f"lses[{i}]", dev) for i, t in enumerate(lses)])
+    rows = 1
+    for x in dims[:-1]:
+        rows *= x
+    op = _sized(out, dims, dt, "out", dev)
+    lp = 0 if lse is None else _sized(lse, dims[:-1], torch.float32, "lse", dev)
+    with torch.cuda.device(dev):
+        st = load_library().deltakv_merge_attention(DKV_F32 if dt == torch.float32 else DKV_BF16, dims[-1], rows, n, po,
+                                                    pl, op, lp, _stream_on(stream, dev))
+    _check(st, "deltakv_merge_attention")
 
 
 class KernelTimer:
