@@ -2,17 +2,68 @@
 #pragma once
 
 #include "kv8_attn_simple.cuh"
-#include "launch.h"
+#include "kv8_stream.cuh"
 
 namespace dkv {
 
+// How many query rows a CTA takes, how many CTAs the device holds at once, and how many key ranges a row is cut into.
+struct Kv8Plan {
+  int tile, slots, nsplit;
+};
+
+static Kv8Plan kv8_plan(const dkv_kv8_shape& sh, int num_seqs, int max_q, int max_ctx) {
+  const int64_t rows = static_cast<int64_t>(max_q) * (sh.num_q_heads / sh.num_kv_heads);
+  Kv8Plan p;
+  if (sh.dtype == DKV_F32)
+    p.tile = kSimpleRows, p.slots = 4 * num_sms();
+  else
+    p.tile = rows <= 8 ? 8 : 16, p.slots = num_sms() * (rows <= 8 ? 2 : 1);
+  const int64_t base = ceil_div64(rows, p.tile) * sh.num_kv_heads * std::max(num_seqs, 1);
+  const int64_t cells = ceil_div64(max_ctx, kKv8CellKeys);
+  const int most = static_cast<int>(std::max<int64_t>(
+      1, std::min<int64_t>(kKv8MaxSplits, ceil_div64(cells, kKv8MinSplitCells))));
+  // waves of CTAs times the length of one, counted in cells; a CTA's start and end cost about as much as 32 cells
+  p.nsplit = 1;
+  double best = 0;
+  for (int n = 1; n <= most; ++n) {
+    const double t = static_cast<double>(ceil_div64(base * n, p.slots)) * (static_cast<double>(cells) / n + 32.0);
+    if (n == 1 || t < best) best = t, p.nsplit = n;
+  }
+  return p;
+}
+
 int kv8_attn_splits(const dkv_kv8_shape& sh, int num_seqs, int64_t total_q, int max_q, int max_ctx) {
-  const int64_t tiles =
-      ceil_div64(static_cast<int64_t>(max_q) * (sh.num_q_heads / sh.num_kv_heads), kSimpleRows) * sh.num_kv_heads *
-      std::max(num_seqs, 1);
-  const int64_t want = ceil_div64(int64_t{8} * num_sms(), std::max<int64_t>(tiles, 1));
-  const int64_t most = ceil_div64(max_ctx, kKv8CellKeys * kKv8MinSplitCells);
-  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, most, int64_t{kKv8MaxSplits}})));
+  return kv8_plan(sh, num_seqs, max_q, max_ctx).nsplit;
+}
+
+// Joins the splits of each row; starts while the attention kernel's last CTAs run.
+template <typename T, int D>
+static dkv_status launch_combine(const Kv8Attn& p, cudaStream_t st) {
+  if (p.nsplit == 1) return DKV_OK;
+  const int64_t rows = p.total_q * p.heads * p.group;
+  return launch_programmatic(kv8_combine_kernel<T, D>, dim3(static_cast<unsigned>(ceil_div64(rows, 512 / D))),
+                             dim3(128), 0, st, p) == cudaSuccess
+             ? DKV_OK
+             : DKV_ERR_CUDA;
+}
+
+template <int D, bool E4M3, int NT>
+static dkv_status attn_stream(const Kv8Attn& p, cudaStream_t st) {
+  constexpr auto kKernel = kv8_stream_kernel<D, E4M3, NT>;
+  if (!ensure_max_dynamic_smem<kKernel, true>()) return DKV_ERR_CUDA;
+  CUtensorMap map;
+  if (!make_map_codes(&map, p.codes, static_cast<uint64_t>(p.num_blocks) * p.heads * 2 * p.block, D)) return DKV_ERR_CUDA;
+  const int row_tiles = static_cast<int>(ceil_div64(static_cast<int64_t>(p.max_q) * p.group, 8 * NT));
+  const int64_t ctas = static_cast<int64_t>(p.nsplit) * row_tiles * p.heads * p.num_seqs;
+  if (ctas > INT32_MAX) return DKV_ERR_UNSUPPORTED;
+  kKernel<<<static_cast<unsigned>(ctas), kStreamWarps * 32, stream_smem<D>(NT), st>>>(map, p, row_tiles);
+  if (cudaGetLastError() != cudaSuccess) return DKV_ERR_CUDA;
+  return launch_combine<__nv_bfloat16, D>(p, st);
+}
+
+template <int D, bool E4M3>
+static dkv_status attn_bf16(const Kv8Attn& p, cudaStream_t st) {
+  return static_cast<int64_t>(p.max_q) * p.group <= 8 ? attn_stream<D, E4M3, 1>(p, st) : attn_stream<D, E4M3, 2>(p, st);
 }
 
 template <typename T, int D, bool E4M3>
@@ -22,11 +73,7 @@ static dkv_status attn_simple(const Kv8Attn& p, cudaStream_t st) {
   if (ctas > INT32_MAX) return DKV_ERR_UNSUPPORTED;
   kv8_attn_simple_kernel<T, D, E4M3><<<static_cast<unsigned>(ctas), 128, 0, st>>>(p, row_tiles);
   if (cudaGetLastError() != cudaSuccess) return DKV_ERR_CUDA;
-  if (p.nsplit > 1) {
-    const int64_t rows = p.total_q * p.heads * p.group;
-    kv8_combine_kernel<T, D><<<static_cast<unsigned>(ceil_div64(rows, 512 / D)), 128, 0, st>>>(p);
-  }
-  return cudaGetLastError() == cudaSuccess ? DKV_OK : DKV_ERR_CUDA;
+  return launch_combine<T, D>(p, st);
 }
 
 dkv_status launch_kv8_attention(const Kv8AttnArgs& a, const Kv8AttnWs& w, void* workspace, cudaStream_t st) {
@@ -52,8 +99,8 @@ dkv_status launch_kv8_attention(const Kv8AttnArgs& a, const Kv8AttnWs& w, void* 
     if (d64) return e4 ? attn_simple<float, 64, true>(p, st) : attn_simple<float, 64, false>(p, st);
     return e4 ? attn_simple<float, 128, true>(p, st) : attn_simple<float, 128, false>(p, st);
   }
-  if (d64) return e4 ? attn_simple<__nv_bfloat16, 64, true>(p, st) : attn_simple<__nv_bfloat16, 64, false>(p, st);
-  return e4 ? attn_simple<__nv_bfloat16, 128, true>(p, st) : attn_simple<__nv_bfloat16, 128, false>(p, st);
+  if (d64) return e4 ? attn_bf16<64, true>(p, st) : attn_bf16<64, false>(p, st);
+  return e4 ? attn_bf16<128, true>(p, st) : attn_bf16<128, false>(p, st);
 }
 
 }  // namespace dkv

@@ -21,6 +21,7 @@ __global__ void __launch_bounds__(128) kv8_attn_simple_kernel(const Kv8Attn a, i
   __shared__ float sfix[kSimpleRows];
   __shared__ int sthere[kSimpleKeys];  // whether the tile's key lies in the context, in a mapped block
   __shared__ float sm[kSimpleRows], sl[kSimpleRows];
+  griddep_launch_dependents();
   int64_t id = blockIdx.x;
   const int split = static_cast<int>(id % a.nsplit);
   id /= a.nsplit;

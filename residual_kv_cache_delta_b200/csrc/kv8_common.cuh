@@ -16,7 +16,7 @@ namespace dkv {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 // The running maximum of a row that has seen no key: finite, so that exp2(-inf - m) is 0 and not NaN.
-constexpr float kNoMax = -1e30f;
+constexpr float kNoMax = -3.0e38f;
 
 struct Kv8Attn {
   const uint8_t* codes;

@@ -120,8 +120,8 @@ def attention(shape, codes, scales, table, q, cu, ctx, scale=0.0, softcap=0.0, w
 
     The kernels' error: a score is a sum of d products in fp32 (d 2^-24 of the sum of magnitudes), then a handful of
     fp32 roundings of the score and its bias (and 2^-20 of the cap); the weights' hardware exponential is off by
-    2^-21, their fp16 rounding (bf16 storage) by 2^-11 of the weight or, below the smallest normal fp16, by 2^-25 of
-    the largest; sums over T keys by T 2^-24; the result by half a step of its type."""
+    2^-21, their fp16 rounding (bf16 storage) by 2^-11 of the weight; what is rounded there is weight times V scale
+    relative to the row's largest such product, so below the smallest normal fp16 by 2^-25 of that, times the code; sums over T keys by T 2^-24; the result by half a step of its type."""
     n, Hq, d = q.shape
     G, B = Hq // shape.num_kv_heads, shape.block_tokens
     sc = scale if scale > 0 else 1.0 / math.sqrt(d)
@@ -165,7 +165,9 @@ def attention(shape, codes, scales, table, q, cu, ctx, scale=0.0, softcap=0.0, w
             half = 2.0 ** -8 if bf else 2.0 ** -24
             t = (2 * e[:, None] + (2.0 ** -11 if bf else 0.0)) * wsum * 1.01 + half * 1.01 * out[rows, h].abs()
             if bf:
-                t = t + 2.0 ** -24 * vv.sum(0)
+                vs = scales[ids, h // G, 1].double().repeat_interleave(B)[:T].nan_to_num(0.0)
+                code = codes[ids, h // G, 1].double().flatten(0, 1)[:T].abs().masked_fill(~see.any(0)[:, None], 0.0)
+                t = t + 2.0 ** -25 * (w.nan_to_num(0.0) * vs).amax(-1, keepdim=True) * code.sum(0)
             tol[rows, h] = t + 1e-30
             tol_l[rows, h] = e + 2.0 ** -22 * lse[rows, h].abs().nan_to_num(0.0, posinf=0.0)
     return out, lse, tol, tol_l
