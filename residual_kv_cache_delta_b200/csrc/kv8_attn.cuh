@@ -2,9 +2,12 @@
 #pragma once
 
 #include "kv8_attn_simple.cuh"
-#include "kv8_stream.cuh"
+#include "kv8_tile.cuh"
 
 namespace dkv {
+
+// Up to so many rows per kv head the streaming kernel is taken, above it the tcgen05 one.
+constexpr int kStreamMaxRows = 16;
 
 // How many query rows a CTA takes, how many CTAs the device holds at once, and how many key ranges a row is cut into.
 struct Kv8Plan {
@@ -16,8 +19,10 @@ static Kv8Plan kv8_plan(const dkv_kv8_shape& sh, int num_seqs, int max_q, int ma
   Kv8Plan p;
   if (sh.dtype == DKV_F32)
     p.tile = kSimpleRows, p.slots = 4 * num_sms();
-  else
+  else if (rows <= kStreamMaxRows)
     p.tile = rows <= 8 ? 8 : 16, p.slots = num_sms() * (rows <= 8 ? 2 : 1);
+  else
+    p.tile = kTileRows, p.slots = num_sms();
   const int64_t base = ceil_div64(rows, p.tile) * sh.num_kv_heads * std::max(num_seqs, 1);
   const int64_t cells = ceil_div64(max_ctx, kKv8CellKeys);
   const int most = static_cast<int>(std::max<int64_t>(
@@ -61,9 +66,26 @@ static dkv_status attn_stream(const Kv8Attn& p, cudaStream_t st) {
   return launch_combine<__nv_bfloat16, D>(p, st);
 }
 
+template <int D, bool E4M3, bool BIAS>
+static dkv_status attn_tile(const Kv8Attn& p, cudaStream_t st) {
+  constexpr auto kKernel = kv8_tile_kernel<D, E4M3, BIAS>;
+  if (!ensure_max_dynamic_smem<kKernel>()) return DKV_ERR_CUDA;
+  CUtensorMap map;
+  if (!make_map_codes(&map, p.codes, static_cast<uint64_t>(p.num_blocks) * p.heads * 2 * p.block, D)) return DKV_ERR_CUDA;
+  const int row_tiles = static_cast<int>(ceil_div64(static_cast<int64_t>(p.max_q) * p.group, kTileRows));
+  const int64_t ctas = static_cast<int64_t>(p.nsplit) * row_tiles * p.heads * p.num_seqs;
+  if (ctas > INT32_MAX) return DKV_ERR_UNSUPPORTED;
+  kKernel<<<static_cast<unsigned>(ctas), kTileThreads, TileSmem<D>::bytes, st>>>(map, p, row_tiles);
+  if (cudaGetLastError() != cudaSuccess) return DKV_ERR_CUDA;
+  return launch_combine<__nv_bfloat16, D>(p, st);
+}
+
 template <int D, bool E4M3>
 static dkv_status attn_bf16(const Kv8Attn& p, cudaStream_t st) {
-  return static_cast<int64_t>(p.max_q) * p.group <= 8 ? attn_stream<D, E4M3, 1>(p, st) : attn_stream<D, E4M3, 2>(p, st);
+  const int64_t rows = static_cast<int64_t>(p.max_q) * p.group;
+  if (rows <= 8) return attn_stream<D, E4M3, 1>(p, st);
+  if (rows <= kStreamMaxRows) return attn_stream<D, E4M3, 2>(p, st);
+  return p.softcap > 0.f || p.slopes ? attn_tile<D, E4M3, true>(p, st) : attn_tile<D, E4M3, false>(p, st);
 }
 
 template <typename T, int D, bool E4M3>

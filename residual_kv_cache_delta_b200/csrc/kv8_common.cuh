@@ -105,9 +105,10 @@ __device__ __forceinline__ Kv8Span kv8_span(const Kv8Seq& s, int window, int p0,
   return v;
 }
 
-// Cells [v0, v1) of split `split`: an even share of the span, at least kKv8MinSplitCells.
-__device__ __forceinline__ void kv8_split(int cells, int nsplit, int split, int& v0, int& v1) {
-  const int per = max((cells + nsplit - 1) / nsplit, nsplit > 1 ? kKv8MinSplitCells : 1);
+// Cells [v0, v1) of split `split`: an even share of the span, at least kKv8MinSplitCells, in multiples of `unit`.
+__device__ __forceinline__ void kv8_split(int cells, int nsplit, int split, int& v0, int& v1, int unit = 1) {
+  int per = max((cells + nsplit - 1) / nsplit, nsplit > 1 ? kKv8MinSplitCells : 1);
+  per = (per + unit - 1) / unit * unit;
   v0 = static_cast<int>(min(static_cast<int64_t>(cells), static_cast<int64_t>(split) * per));
   v1 = min(cells, v0 + per);
 }
