@@ -8,8 +8,10 @@ raises ``RuntimeError``.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 from dataclasses import dataclass
+from functools import cached_property
 from typing import Optional
 
 import torch
@@ -405,14 +407,14 @@ class KV8Shape:
     dtype: torch.dtype = torch.bfloat16
     code: str = "int8"
 
-    @property
+    @cached_property
     def c(self) -> DkvKv8Shape:
         if self.dtype not in (torch.bfloat16, torch.float32) or self.code not in KV8_CODES:
             raise ValueError(f"KV8Shape: dtype {self.dtype}, code {self.code!r}")
         return DkvKv8Shape(self.num_q_heads, self.num_kv_heads, self.head_dim, self.block_tokens,
                            DKV_F32 if self.dtype == torch.float32 else DKV_BF16, KV8_CODES[self.code])
 
-    @property
+    @cached_property
     def code_dtype(self) -> torch.dtype:
         return torch.int8 if self.code == "int8" else torch.float8_e4m3fn
 
@@ -453,37 +455,47 @@ def kv8_attention_workspace(shape: KV8Shape, num_seqs: int, total_q: int, max_q:
     return n.value
 
 
-def _sized(t: torch.Tensor, dims: tuple, dtype: torch.dtype, name: str, dev: torch.device) -> int:
-    """Pointer of a contiguous tensor of exactly these dimensions on ``dev``."""
-    if tuple(t.shape) != tuple(dims):
-        raise ValueError(f"{name} must have shape {tuple(dims)}, got {tuple(t.shape)}")
-    if t.device != dev:
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    return _ptr(t, dtype, name)
+def _refuse(t, dims: tuple, dtype: torch.dtype, name: str, dev: int):
+    if not t.is_cuda or t.get_device() != dev:
+        raise ValueError(f"{name} must be on {'a GPU' if dev < 0 else f'cuda:{dev}'}, got {t.device}")
+    if t.shape != dims:
+        raise ValueError(f"{name} must have shape {dims}, got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _rows(t: torch.Tensor, n: int, heads: int, shape: KV8Shape, name: str, dev: torch.device) -> tuple[int, int]:
+def _sized(t: torch.Tensor, dims: tuple, dtype: torch.dtype, name: str, dev: int) -> int:
+    """Pointer of a contiguous tensor of exactly these dimensions on GPU ``dev``."""
+    if dev < 0 or t.get_device() != dev or t.shape != dims or t.dtype is not dtype or not t.is_contiguous():
+        _refuse(t, dims, dtype, name, dev)
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, n: int, heads: int, shape: KV8Shape, name: str, dev: int) -> tuple[int, int]:
     """Pointer and row stride of [n, heads, d] whose rows may lie apart (a view of a fused projection)."""
-    if tuple(t.shape) != (n, heads, shape.head_dim):
-        raise ValueError(f"{name} must have shape {(n, heads, shape.head_dim)}, got {tuple(t.shape)}")
-    if t.device != dev or not t.is_cuda:
-        raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    if t.dtype != shape.dtype:
-        raise ValueError(f"{name} must be {shape.dtype}, got {t.dtype}")
-    if n > 0 and (t.stride(2) != 1 or (heads > 1 and t.stride(1) != shape.head_dim)):
+    d = shape.head_dim
+    if dev < 0 or t.get_device() != dev or t.shape != (n, heads, d) or t.dtype is not shape.dtype:
+        _refuse(t, (n, heads, d), shape.dtype, name, dev)
+    st = t.stride()
+    if n > 0 and (st[2] != 1 or (heads > 1 and st[1] != d)):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return t.data_ptr(), (t.stride(0) if n > 1 else heads * shape.head_dim)
+    return t.data_ptr(), (st[0] if n > 1 else heads * d)
 
 
-def _kv8_cache(shape: KV8Shape, cache: KV8Cache) -> DkvKv8Cache:
-    nb, H, B, d = cache.num_blocks, shape.num_kv_heads, shape.block_tokens, shape.head_dim
-    dev = cache.codes.device
-    return DkvKv8Cache(_sized(cache.codes, (nb, H, 2, B, d), shape.code_dtype, "cache.codes", dev),
+def _kv8_cache(shape: KV8Shape, cache: KV8Cache, dev: int) -> DkvKv8Cache:
+    codes, H = cache.codes, shape.num_kv_heads
+    nb = codes.shape[0]
+    return DkvKv8Cache(_sized(codes, (nb, H, 2, shape.block_tokens, shape.head_dim), shape.code_dtype, "cache.codes", dev),
                        _sized(cache.scales, (nb, H, 2), torch.float32, "cache.scales", dev), nb)
 
 
-def _stream_on(stream, dev: torch.device) -> int:
-    return torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
+def _call_on(dev: int, stream, fn, *args) -> int:
+    """fn(*args, stream) with GPU ``dev`` current; its current stream unless one is given."""
+    if torch.cuda.current_device() == dev:
+        return fn(*args, torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream))
+    with torch.cuda.device(dev):
+        return fn(*args, torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream))
 
 
 def deltakv_kv8_append(shape: KV8Shape, cache: KV8Cache, k_new: torch.Tensor, v_new: torch.Tensor,
@@ -494,16 +506,17 @@ def deltakv_kv8_append(shape: KV8Shape, cache: KV8Cache, k_new: torch.Tensor, v_
     """Enqueue ``deltakv_kv8_append``.  k_new/v_new [total_new, H_kv, d] (rows may be strided); cu_new [num_seqs+1],
     start_pos [num_seqs], block_tables [num_seqs, max_blocks] int32; rope [max_pos, rot_dim] fp32 (cosines, then
     sines); positions [total_new] int32 or None; q [total_new, H_q, d] with q_out of the same shape, or None."""
-    dev, n = cache.codes.device, k_new.shape[0]
-    cs, cc = shape.c, _kv8_cache(shape, cache)
+    dev, n = cache.codes.get_device(), k_new.shape[0]
+    cc = _kv8_cache(shape, cache, dev)
     num_seqs, max_blocks = block_tables.shape
     kp, ks = _rows(k_new, n, shape.num_kv_heads, shape, "k_new", dev)
     vp, vs = _rows(v_new, n, shape.num_kv_heads, shape, "v_new", dev)
     qp, qs, qo, cr = 0, 0, 0, None
     if rope is not None:
-        cr = DkvKv8Rope(_sized(rope, rope.shape, torch.float32, "rope", dev),
-                        _sized(positions, (n,), torch.int32, "positions", dev) if positions is not None else 0,
-                        rope.shape[0], rope.shape[1], int(rope_pairs))
+        max_pos, rot = rope.shape
+        pp = 0 if positions is None else _sized(positions, (n,), torch.int32, "positions", dev)
+        cr = ctypes.byref(DkvKv8Rope(_sized(rope, (max_pos, rot), torch.float32, "rope", dev), pp, max_pos, rot,
+                                     int(rope_pairs)))
     elif positions is not None:
         raise ValueError("positions without rope")
     if (q is None) != (q_out is None):
@@ -511,13 +524,11 @@ def deltakv_kv8_append(shape: KV8Shape, cache: KV8Cache, k_new: torch.Tensor, v_
     if q is not None:
         qp, qs = _rows(q, n, shape.num_q_heads, shape, "q", dev)
         qo = _sized(q_out, (n, shape.num_q_heads, shape.head_dim), shape.dtype, "q_out", dev)
-    with torch.cuda.device(dev):
-        st = load_library().deltakv_kv8_append(
-            ctypes.byref(cs), ctypes.byref(cc), ctypes.byref(cr) if cr is not None else None, kp, ks, vp, vs,
-            _sized(cu_new, (num_seqs + 1,), torch.int32, "cu_new", dev),
-            _sized(start_pos, (num_seqs,), torch.int32, "start_pos", dev),
-            _sized(block_tables, block_tables.shape, torch.int32, "block_tables", dev), max_blocks, num_seqs, n, max_new,
-            qp, qs, qo, _stream_on(stream, dev))
+    st = _call_on(dev, stream, load_library().deltakv_kv8_append, ctypes.byref(shape.c), ctypes.byref(cc), cr, kp, ks, vp,
+                  vs, _sized(cu_new, (num_seqs + 1,), torch.int32, "cu_new", dev),
+                  _sized(start_pos, (num_seqs,), torch.int32, "start_pos", dev),
+                  _sized(block_tables, (num_seqs, max_blocks), torch.int32, "block_tables", dev), max_blocks, num_seqs, n,
+                  max_new, qp, qs, qo)
     _check(st, "deltakv_kv8_append")
 
 
@@ -530,51 +541,44 @@ def deltakv_kv8_attention(shape: KV8Shape, cache: KV8Cache, q: torch.Tensor, cu_
     """Enqueue ``deltakv_kv8_attention``.  q [total_q, H_q, d] (rows may be strided), out the same shape, lse [total_q,
     H_q] fp32 or None; cu_q [num_seqs+1] or None (one query token per sequence), context_lens [num_seqs], block_tables
     [num_seqs, max_blocks] int32; alibi_slopes [H_q] fp32, prefix_lens [num_seqs] and first_key [total_q] int32."""
-    dev, n = cache.codes.device, q.shape[0]
-    cs, cc = shape.c, _kv8_cache(shape, cache)
+    dev, n = cache.codes.get_device(), q.shape[0]
+    cc, i32, f32 = _kv8_cache(shape, cache, dev), torch.int32, torch.float32
     num_seqs, max_blocks = block_tables.shape
-    qp, qs = _rows(q, n, shape.num_q_heads, shape, "q", dev)
-
-    def opt(t, dims, dtype, name):
-        return 0 if t is None else _sized(t, dims, dtype, name, dev)
-
-    score = DkvKv8Score(float(softcap), int(window),
-                        opt(alibi_slopes, (shape.num_q_heads,), torch.float32, "alibi_slopes"),
-                        opt(prefix_lens, (num_seqs,), torch.int32, "prefix_lens"),
-                        opt(first_key, (n,), torch.int32, "first_key"))
-    ws = opt(workspace, (workspace.numel(),) if workspace is not None else (), torch.uint8, "workspace")
-    with torch.cuda.device(dev):
-        st = load_library().deltakv_kv8_attention(
-            ctypes.byref(cs), ctypes.byref(cc), ctypes.byref(score), qp, qs,
-            opt(cu_q, (num_seqs + 1,), torch.int32, "cu_q"),
-            _sized(context_lens, (num_seqs,), torch.int32, "context_lens", dev),
-            _sized(block_tables, block_tables.shape, torch.int32, "block_tables", dev), max_blocks, num_seqs, n, max_q,
-            max_ctx, float(softmax_scale),
-            _sized(out, (n, shape.num_q_heads, shape.head_dim), shape.dtype, "out", dev),
-            opt(lse, (n, shape.num_q_heads), torch.float32, "lse"), ws,
-            workspace.numel() if workspace is not None else 0, _stream_on(stream, dev))
+    H = shape.num_q_heads
+    qp, qs = _rows(q, n, H, shape, "q", dev)
+    score = None
+    if softcap or window or alibi_slopes is not None or prefix_lens is not None or first_key is not None:
+        score = ctypes.byref(DkvKv8Score(
+            softcap, window, 0 if alibi_slopes is None else _sized(alibi_slopes, (H,), f32, "alibi_slopes", dev),
+            0 if prefix_lens is None else _sized(prefix_lens, (num_seqs,), i32, "prefix_lens", dev),
+            0 if first_key is None else _sized(first_key, (n,), i32, "first_key", dev)))
+    wsn = 0 if workspace is None else workspace.numel()
+    st = _call_on(dev, stream, load_library().deltakv_kv8_attention, ctypes.byref(shape.c), ctypes.byref(cc), score, qp,
+                  qs, 0 if cu_q is None else _sized(cu_q, (num_seqs + 1,), i32, "cu_q", dev),
+                  _sized(context_lens, (num_seqs,), i32, "context_lens", dev),
+                  _sized(block_tables, (num_seqs, max_blocks), i32, "block_tables", dev), max_blocks, num_seqs, n, max_q,
+                  max_ctx, softmax_scale, _sized(out, (n, H, shape.head_dim), shape.dtype, "out", dev),
+                  0 if lse is None else _sized(lse, (n, H), f32, "lse", dev),
+                  0 if workspace is None else _sized(workspace, (wsn,), torch.uint8, "workspace", dev), wsn)
     _check(st, "deltakv_kv8_attention")
 
 
 def deltakv_merge_attention(outs, lses, out: torch.Tensor, lse: Optional[torch.Tensor], stream=None) -> None:
     """Enqueue ``deltakv_merge_attention``: outs, lses are lists of [..., d] and [...] (fp32) tensors, the results of
     the same queries over disjoint keys (deltakv_decode_attention*, deltakv_kv8_attention); out/lse of the same shapes."""
-    if len(outs) != len(lses) or not 1 <= len(outs) <= MERGE_MAX_PARTS:
-        raise ValueError(f"1 to {MERGE_MAX_PARTS} parts, as many lses as outs: got {len(outs)} and {len(lses)}")
-    dev, dims, dt = out.device, tuple(out.shape), out.dtype
-    if dt not in (torch.bfloat16, torch.float32) or len(dims) < 1:
-        raise ValueError(f"out: {dt} of shape {dims}")
     n = len(outs)
-    po = (ctypes.c_void_p * n)(*[_sized(t, dims, dt, f"outs[{i}]", dev) for i, t in enumerate(outs)])
-    pl = (ctypes.c_void_p * n)(*[_sized(t, dims[:-1], torch.float32, f"lses[{i}]", dev) for i, t in enumerate(lses)])
-    rows = 1
-    for x in dims[:-1]:
-        rows *= x
-    op = _sized(out, dims, dt, "out", dev)
-    lp = 0 if lse is None else _sized(lse, dims[:-1], torch.float32, "lse", dev)
-    with torch.cuda.device(dev):
-        st = load_library().deltakv_merge_attention(DKV_F32 if dt == torch.float32 else DKV_BF16, dims[-1], rows, n, po,
-                                                    pl, op, lp, _stream_on(stream, dev))
+    if len(lses) != n or not 1 <= n <= MERGE_MAX_PARTS:
+        raise ValueError(f"1 to {MERGE_MAX_PARTS} parts, as many lses as outs: got {n} and {len(lses)}")
+    dev, dims, dt, f32 = out.get_device(), tuple(out.shape), out.dtype, torch.float32
+    if dt not in (torch.bfloat16, f32) or not dims:
+        raise ValueError(f"out: {dt} of shape {dims}")
+    rdims = dims[:-1]
+    P = ctypes.c_void_p * n
+    po = P(*[_sized(t, dims, dt, "outs", dev) for t in outs])
+    pl = P(*[_sized(t, rdims, f32, "lses", dev) for t in lses])
+    st = _call_on(dev, stream, load_library().deltakv_merge_attention, DKV_F32 if dt is f32 else DKV_BF16, dims[-1],
+                  math.prod(rdims), n, po, pl, _sized(out, dims, dt, "out", dev),
+                  0 if lse is None else _sized(lse, rdims, f32, "lse", dev))
     _check(st, "deltakv_merge_attention")
 
 
