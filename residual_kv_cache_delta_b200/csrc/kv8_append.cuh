@@ -1,9 +1,10 @@
 // Append to the 8-bit paged cache: position rotation of K (and q), quantisation, paged write.
 //
-// A CTA owns one block of one sequence and walks kv heads; a thread owns 16 dimensions of one row ("unit") of K and
-// of V, so that a block's largest magnitude is one reduction over registers and each input value is read once.
-// Unit u of a rotated row holds the dimensions whose partners it also holds: 8u .. 8u+7 of the first half and of
-// the second (halves), or 16u .. 16u+15 (pairs); both use entries 8u .. 8u+7 of the cosines and sines.
+// Bound by memory: every input value is read once and every code written once.  A CTA owns K or V of one block of one
+// sequence and walks kv heads; a thread owns 16 dimensions of one row ("unit"), so that a block's largest magnitude is a
+// reduction over registers, and loads several heads at once, before anything that it does not need for their addresses.
+// Unit u of a rotated row holds dimensions whose partners it also holds: 8u .. 8u+7 of the first half and of the second
+// (halves), or 16u .. 16u+15 (pairs); both use entries 8u .. 8u+7 of the cosines and sines, which stay in registers.
 #pragma once
 
 #include "kv8_common.cuh"
@@ -34,31 +35,50 @@ struct Kv8Append {
   int head_steps;      // kv heads a CTA walks
   int64_t kv_ctas;
   int q_head_steps;    // q heads a thread walks
+  float neg_zero;      // -0, not known to the compiler
 };
 
+// Eight values of type T as they lie in memory.
 template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&f)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    unpack16(*reinterpret_cast<const uint4*>(p), f, static_cast<__nv_bfloat16*>(nullptr));
-  } else {
-    const float4 x = reinterpret_cast<const float4*>(p)[0], y = reinterpret_cast<const float4*>(p)[1];
-    f[0] = x.x, f[1] = x.y, f[2] = x.z, f[3] = x.w, f[4] = y.x, f[5] = y.y, f[6] = y.z, f[7] = y.w;
+struct Oct;
+template <>
+struct Oct<float> {
+  float4 v, w;
+  __device__ __forceinline__ void get(float* f) const {
+    f[0] = v.x, f[1] = v.y, f[2] = v.z, f[3] = v.w, f[4] = w.x, f[5] = w.y, f[6] = w.z, f[7] = w.w;
   }
-}
-template <typename T>
-__device__ __forceinline__ void store8(T* p, const float (&f)[8]) {
-  if constexpr (sizeof(T) == 2) {
-    __nv_bfloat162 w[4];
+  static __device__ __forceinline__ Oct make(const float* f) {
+    return {make_float4(f[0], f[1], f[2], f[3]), make_float4(f[4], f[5], f[6], f[7])};
+  }
+};
+template <>
+struct Oct<__nv_bfloat16> {
+  uint4 v;
+  __device__ __forceinline__ void get(float* f) const {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-    for (int j = 0; j < 4; ++j) w[j] = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
-    *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(w);
-  } else {
-    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    for (int j = 0; j < 4; ++j) f[2 * j] = __uint_as_float(w[j] << 16), f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
   }
+  static __device__ __forceinline__ Oct make(const float* f) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const __nv_bfloat162 x = __floats2bfloat162_rn(f[2 * j], f[2 * j + 1]);
+      w[j] = *reinterpret_cast<const uint32_t*>(&x);
+    }
+    return {make_uint4(w[0], w[1], w[2], w[3])};
+  }
+};
+template <typename T>
+struct Unit {
+  Oct<T> a, b;
+};
+template <typename T>
+__device__ __forceinline__ Unit<T> load_unit(const T* p, int da, int db) {
+  return {*reinterpret_cast<const Oct<T>*>(p + da), *reinterpret_cast<const Oct<T>*>(p + db)};
 }
 
-// First dimensions of the two 8-wide halves of unit u.
+// First dimensions of the two octets of unit u.
 template <bool PAIRS>
 __device__ __forceinline__ void unit_dims(int u, int rot, int& a, int& b) {
   if (PAIRS || u * 16 >= rot) {
@@ -70,78 +90,115 @@ __device__ __forceinline__ void unit_dims(int u, int rot, int& a, int& b) {
   }
 }
 
-// Rotates a unit; products and sums are rounded one by one, so that the result does not depend on contraction.
+// Two fp32 operations to an instruction.  A product is a fused multiply-add of -0 that the compiler does not know (nz, from
+// the kernel's arguments): it is rounded by itself, where a packed product is contracted with the sum behind it.
+__device__ __forceinline__ uint64_t pack2(float x, float y) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Rotates a unit; products and sums are rounded one by one.
 template <bool PAIRS>
-__device__ __forceinline__ void rotate_unit(float (&x)[8], float (&y)[8], const float (&c)[8], const float (&s)[8]) {
-  if (PAIRS) {
+__device__ __forceinline__ void rotate_unit(float (&x)[16], const float (&cs)[16], uint64_t nz) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float& a = j < 4 ? x[2 * j] : y[2 * j - 8];
-      float& b = j < 4 ? x[2 * j + 1] : y[2 * j - 7];
-      const float ra = __fsub_rn(__fmul_rn(a, c[j]), __fmul_rn(b, s[j]));
-      const float rb = __fadd_rn(__fmul_rn(b, c[j]), __fmul_rn(a, s[j]));
-      a = ra, b = rb;
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float ra = __fsub_rn(__fmul_rn(x[j], c[j]), __fmul_rn(y[j], s[j]));
-      const float rb = __fadd_rn(__fmul_rn(y[j], c[j]), __fmul_rn(x[j], s[j]));
-      x[j] = ra, y[j] = rb;
-    }
+  for (int j = 0; j < 8; j += 2) {
+    float &a0 = PAIRS ? x[2 * j] : x[j], &a1 = PAIRS ? x[2 * j + 2] : x[j + 1];
+    float &b0 = PAIRS ? x[2 * j + 1] : x[8 + j], &b1 = PAIRS ? x[2 * j + 3] : x[9 + j];
+    const uint64_t a = pack2(a0, a1), b = pack2(b0, b1), c = pack2(cs[j], cs[j + 1]), s = pack2(cs[8 + j], cs[9 + j]);
+    unpack2(fma2(fma2(b, s, nz), pack2(-1.f, -1.f), fma2(a, c, nz)), a0, a1);
+    unpack2(add2(fma2(b, c, nz), fma2(a, s, nz)), b0, b1);
   }
 }
 
 // Cosines and sines 8u .. 8u+7 of a token; false when the unit is not rotated.  A position outside the table is
 // recorded and leaves the row unrotated.
-__device__ __forceinline__ bool load_angles(const Kv8Append& a, int pos, int u, float (&c)[8], float (&s)[8]) {
+__device__ __forceinline__ bool load_angles(const Kv8Append& a, int pos, int u, float (&cs)[16]) {
   if (u * 16 >= a.rot) return false;
   if (pos < 0 || pos >= a.max_pos) {
     record_error(DKV_DEVERR_BOUNDS);
     return false;
   }
   const float* t = a.rope + static_cast<int64_t>(pos) * a.rot + 8 * u;
-  load8(t, c);
-  load8(t + a.rot / 2, s);
+  reinterpret_cast<const Oct<float>*>(t)->get(cs);
+  reinterpret_cast<const Oct<float>*>(t + a.rot / 2)->get(cs + 8);
   return true;
 }
 
-__device__ __forceinline__ uint32_t max_bits(uint32_t m, const float (&f)[8]) {
-#pragma unroll
-  for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(f[j]) & 0x7fffffffu);
-  return m;
-}
-
-// 8 codes of f * inv, round to nearest even, saturating.
+// 8 codes of f * inv, round to nearest even.  |f * inv| exceeds the largest code by a few roundings at most, so that the
+// nearest int8 code is in range without a clamp.
 template <bool E4M3>
-__device__ __forceinline__ uint2 quantise8(const float (&f)[8], float inv) {
-  uint32_t w[2] = {0, 0};
-  if constexpr (E4M3) {
+__device__ __forceinline__ uint2 quantise8(const float* f, float inv, uint64_t nz) {
+  const uint64_t i2 = pack2(inv, inv);
+  uint32_t w[2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t p = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * j] * inv, f[2 * j + 1] * inv), __NV_SATFINITE,
-                                                  __NV_E4M3);
-      w[j / 2] |= p << (16 * (j % 2));
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int c = __float2int_rn(fminf(fmaxf(f[j] * inv, -127.f), 127.f));
-      w[j / 4] |= (static_cast<uint32_t>(c) & 0xffu) << (8 * (j % 4));
+  for (int h = 0; h < 2; ++h) {
+    const uint64_t y0 = fma2(pack2(f[4 * h], f[4 * h + 1]), i2, nz), y1 = fma2(pack2(f[4 * h + 2], f[4 * h + 3]), i2, nz);
+    float v[4];
+    if constexpr (E4M3) {
+      uint16_t lo, hi;
+      unpack2(y0, v[0], v[1]), unpack2(y1, v[2], v[3]);
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(v[1]), "f"(v[0]));
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(v[3]), "f"(v[2]));
+      w[h] = static_cast<uint32_t>(lo) | static_cast<uint32_t>(hi) << 16;
+    } else {  // adding 1.5 2^23 leaves the rounded integer in the low mantissa bits
+      const uint64_t magic = pack2(12582912.f, 12582912.f);
+      unpack2(add2(y0, magic), v[0], v[1]), unpack2(add2(y1, magic), v[2], v[3]);
+      w[h] = __byte_perm(__byte_perm(__float_as_uint(v[0]), __float_as_uint(v[1]), 0x0040),
+                         __byte_perm(__float_as_uint(v[2]), __float_as_uint(v[3]), 0x0040), 0x5410);
     }
   }
   return make_uint2(w[0], w[1]);
 }
+__device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
 
-template <typename T, int D, bool E4M3, bool PAIRS>
+// Heads of a thread's loads in flight (32 registers)
+template <typename T>
+constexpr int kAppendHeads = sizeof(T) == 2 ? 4 : 2;
+
+// Loads the unit of the next heads from h on (those below h1).
+template <typename T, int D>
+__device__ __forceinline__ void load_heads(const T* src, int h, int h1, int da, int db, bool on,
+                                           Unit<T> (&x)[kAppendHeads<T>]) {
+#pragma unroll
+  for (int i = 0; i < kAppendHeads<T>; ++i) {
+    x[i] = Unit<T>{};
+    if (on && h + i < h1) x[i] = load_unit(src + (h + i) * D, da, db);
+  }
+}
+
+template <typename T, int D, bool PAIRS>
 __device__ __forceinline__ void append_q(const Kv8Append& a, int64_t cta) {
-  constexpr int kUnits = D / 16;
+  constexpr int kUnits = D / 16, kN = kAppendHeads<T>;
   const int per = blockDim.x / kUnits;  // tokens of a CTA
   const int chunks = (a.q_heads + a.q_head_steps - 1) / a.q_head_steps;
-  const int h0 = static_cast<int>(cta % chunks) * a.q_head_steps;
+  const int h0 = static_cast<int>(cta % chunks) * a.q_head_steps, h1 = min(h0 + a.q_head_steps, a.q_heads);
   const int64_t tok = cta / chunks * per + threadIdx.x / kUnits;
   if (tok >= a.total_new) return;
   const int u = threadIdx.x % kUnits;
+  int da, db;
+  unit_dims<PAIRS>(u, a.rot, da, db);
+  const T* src = static_cast<const T*>(a.q) + tok * a.q_stride;
+  T* dst = static_cast<T*>(a.q_out) + tok * a.q_heads * D;
+  Unit<T> raw[kN];
+  load_heads<T, D>(src, h0, h1, da, db, true, raw);
   int lo = 0, hi = a.num_seqs;  // the last sequence that begins at or before the token
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -149,33 +206,36 @@ __device__ __forceinline__ void append_q(const Kv8Append& a, int64_t cta) {
   }
   if (tok < a.cu_new[lo] || tok >= a.cu_new[lo + 1]) return;  // a row of no sequence
   const int pos = a.positions ? a.positions[tok] : a.start_pos[lo] + static_cast<int>(tok - a.cu_new[lo]);
-  float c[8], s[8], x[8], y[8];
-  const bool turn = load_angles(a, pos, u, c, s);
-  int da, db;
-  unit_dims<PAIRS>(u, a.rot, da, db);
-  const T* src = static_cast<const T*>(a.q) + tok * a.q_stride;
-  T* dst = static_cast<T*>(a.q_out) + tok * a.q_heads * D;
-  for (int h = h0; h < min(h0 + a.q_head_steps, a.q_heads); ++h) {
-    load8(src + h * D + da, x);
-    load8(src + h * D + db, y);
-    if (turn) rotate_unit<PAIRS>(x, y, c, s);
-    store8(dst + h * D + da, x);
-    store8(dst + h * D + db, y);
+  float cs[16], x[16];
+  const uint64_t nz = pack2(a.neg_zero, a.neg_zero);
+  const bool turn = load_angles(a, pos, u, cs);
+  for (int h = h0; h < h1; h += kN) {
+    if (h > h0) load_heads<T, D>(src, h, h1, da, db, true, raw);
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      if (h + i >= h1) continue;
+      raw[i].a.get(x), raw[i].b.get(x + 8);
+      if (turn) rotate_unit<PAIRS>(x, cs, nz);
+      *reinterpret_cast<Oct<T>*>(dst + (h + i) * D + da) = Oct<T>::make(x);
+      *reinterpret_cast<Oct<T>*>(dst + (h + i) * D + db) = Oct<T>::make(x + 8);
+    }
   }
 }
 
 template <typename T, int D, bool E4M3, bool PAIRS>
-__global__ void __launch_bounds__(512) kv8_append_kernel(const Kv8Append a) {
-  constexpr int kUnits = D / 16;
+__global__ void __maxnreg__(72) kv8_append_kernel(const __grid_constant__ Kv8Append a) {
+  constexpr int kUnits = D / 16, kN = kAppendHeads<T>;
   constexpr float kTop = E4M3 ? 448.0f : 127.0f;
-  __shared__ uint2 top[2][16];
+  __shared__ uint32_t tops[2][kN][16];
   if (blockIdx.x >= a.kv_ctas) {
-    append_q<T, D, E4M3, PAIRS>(a, blockIdx.x - a.kv_ctas);
+    append_q<T, D, PAIRS>(a, blockIdx.x - a.kv_ctas);
     return;
   }
   const int steps = (a.heads + a.head_steps - 1) / a.head_steps;
   int64_t id = blockIdx.x;
-  const int h0 = static_cast<int>(id % steps) * a.head_steps;
+  const int half = static_cast<int>(id & 1);  // 0: K, 1: V
+  id >>= 1;
+  const int h0 = static_cast<int>(id % steps) * a.head_steps, h1 = min(h0 + a.head_steps, a.heads);
   id /= steps;
   const int nth = static_cast<int>(id % a.blocks_per_seq), s = static_cast<int>(id / a.blocks_per_seq);
   const int row0 = a.cu_new[s], n = a.cu_new[s + 1] - row0, start = a.start_pos[s];
@@ -187,86 +247,67 @@ __global__ void __launch_bounds__(512) kv8_append_kernel(const Kv8Append a) {
   }
   const int b = start / a.block + nth;
   if (static_cast<int64_t>(b) * a.block >= static_cast<int64_t>(start) + n) return;
-  const int blk = kv8_block(a.block_tables, a.max_blocks, a.num_blocks, s, b);
-  if (blk < 0) return;
   const int u = threadIdx.x % kUnits, r = threadIdx.x / kUnits;
   const int at = b * a.block + r - start;  // row of this call, or before (< 0) or after (>= n) its rows
   const bool fresh = at >= 0 && at < n;
   const bool held = b * a.block < start;   // the block holds earlier rows
   const int64_t tok = row0 + (fresh ? at : 0);
-  float c[8], sn[8];
+  int da = 16 * u, db = 16 * u + 8;
+  if (half == 0) unit_dims<PAIRS>(u, a.rot, da, db);
+  const T* src = half ? static_cast<const T*>(a.v) + tok * a.v_stride : static_cast<const T*>(a.k) + tok * a.k_stride;
+  Unit<T> raw[kN];
+  load_heads<T, D>(src, h0, h1, da, db, fresh, raw);
+  const int blk = kv8_block(a.block_tables, a.max_blocks, a.num_blocks, s, b);
+  if (blk < 0) return;
+  float cs[16];
+  const uint64_t nz = pack2(a.neg_zero, a.neg_zero);
   bool turn = false;
-  int da, db;
-  unit_dims<PAIRS>(u, a.rot, da, db);
-  if (fresh && a.rot > 0) turn = load_angles(a, a.positions ? a.positions[tok] : start + at, u, c, sn);
-  const T* kp = static_cast<const T*>(a.k) + tok * a.k_stride;
-  const T* vp = static_cast<const T*>(a.v) + tok * a.v_stride;
-  const int warps = blockDim.x / 32, warp = threadIdx.x / 32;
-  for (int h = h0; h < min(h0 + a.head_steps, a.heads); ++h) {
-    float kx[8] = {}, ky[8] = {}, vx[8] = {}, vy[8] = {};
-    if (fresh) {
-      load8(kp + h * D + da, kx);
-      load8(kp + h * D + db, ky);
-      load8(vp + h * D + 16 * u, vx);
-      load8(vp + h * D + 16 * u + 8, vy);
-      if (turn) rotate_unit<PAIRS>(kx, ky, c, sn);
-    }
-    // bit patterns of magnitudes order like the magnitudes, with infinities and then NaN on top
-    const uint32_t km = __reduce_max_sync(~0u, max_bits(max_bits(0u, kx), ky));
-    const uint32_t vm = __reduce_max_sync(~0u, max_bits(max_bits(0u, vx), vy));
-    uint2* t = top[(h - h0) & 1];
-    if (threadIdx.x % 32 == 0) t[warp] = make_uint2(km, vm);
-    __syncthreads();
-    uint32_t m[2] = {0u, 0u};
-    for (int w = 0; w < warps; ++w) {
-      const uint2 x = t[w];
-      m[0] = max(m[0], x.x), m[1] = max(m[1], x.y);
-    }
-    const int64_t cell = (static_cast<int64_t>(blk) * a.heads + h) * 2;
-    float inv[2], ratio[2], now[2];
-    bool bad[2], grew[2];
+  if (half == 0 && fresh && a.rot > 0) turn = load_angles(a, a.positions ? a.positions[tok] : start + at, u, cs);
+  const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  int slot = 0;
+  for (int h = h0; h < h1; h += kN, slot ^= 1) {
+    if (h > h0) load_heads<T, D>(src, h, h1, da, db, fresh, raw);
+    float x[16], old[kN];
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      now[j] = fmaxf(__uint_as_float(m[j]), kKv8Floor) * (1.0f / kTop);
-      bad[j] = m[j] >= 0x7f800000u;  // a value is not finite: the block reads as NaN from here on
-      float old = 0.f;
-      if (held) {
-        old = a.scales[cell + j];
-        bad[j] |= !(fabsf(old) <= 3.402823466e38f);
-        now[j] = fmaxf(now[j], old);
-      }
-      grew[j] = held && now[j] > old;
-      inv[j] = __frcp_rn(now[j]);
-      ratio[j] = __fmul_rn(old, inv[j]);
-      if (bad[j]) now[j] = __uint_as_float(0x7fc00000u), inv[j] = 0.f;
-    }
-    uint8_t* kc = a.codes + (cell * a.block + r) * D;
-    uint8_t* vc = kc + static_cast<int64_t>(a.block) * D;
-    if (fresh) {
-      *reinterpret_cast<uint2*>(kc + da) = bad[0] ? make_uint2(0u, 0u) : quantise8<E4M3>(kx, inv[0]);
-      *reinterpret_cast<uint2*>(kc + db) = bad[0] ? make_uint2(0u, 0u) : quantise8<E4M3>(ky, inv[0]);
-      const uint2 x = bad[1] ? make_uint2(0u, 0u) : quantise8<E4M3>(vx, inv[1]);
-      const uint2 y = bad[1] ? make_uint2(0u, 0u) : quantise8<E4M3>(vy, inv[1]);
-      *reinterpret_cast<uint4*>(vc + 16 * u) = make_uint4(x.x, x.y, y.x, y.y);
-    } else if (at < 0) {  // an earlier row: its codes follow a scale that grew
+    for (int i = 0; i < kN; ++i) {
+      old[i] = 0.f;
+      if (held && h + i < h1) old[i] = a.scales[(static_cast<int64_t>(blk) * a.heads + h + i) * 2 + half];
+      raw[i].a.get(x), raw[i].b.get(x + 8);
+      if (turn) rotate_unit<PAIRS>(x, cs, nz);
+      float top = fabsf(x[0]);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        if (bad[j] || !grew[j]) continue;
-        uint8_t* p = (j ? vc : kc) + 16 * u;
-        const uint4 w = *reinterpret_cast<const uint4*>(p);
+      for (int j = 1; j < 16; ++j) top = max_nan(top, fabsf(x[j]));
+      // bit patterns of magnitudes order like the magnitudes, with infinities and then NaN on top
+      const uint32_t m = __reduce_max_sync(~0u, __float_as_uint(top) & 0x7fffffffu);
+      if (lane == 0) tops[slot][i][warp] = m;
+    }
+    __syncthreads();  // also: every thread has read the old scales
+#pragma unroll
+    for (int i = 0; i < kN; ++i) {
+      if (h + i >= h1) continue;
+      const uint32_t m = __reduce_max_sync(~0u, lane < warps ? tops[slot][i][lane] : 0u);
+      const int64_t cell = (static_cast<int64_t>(blk) * a.heads + h + i) * 2 + half;
+      const float now = fmaxf(fmaxf(__uint_as_float(m), kKv8Floor) * (1.0f / kTop), old[i]);
+      // a value is not finite: the block reads as NaN from here on
+      const bool bad = m >= 0x7f800000u || !(fabsf(old[i]) <= 3.402823466e38f);
+      const float inv = __frcp_rn(now);
+      uint8_t* codes = a.codes + (cell * a.block + r) * D;
+      if (fresh) {  // rotated once more: cheaper than to keep the fp32 values of four heads
+        raw[i].a.get(x), raw[i].b.get(x + 8);
+        if (turn) rotate_unit<PAIRS>(x, cs, nz);
+        *reinterpret_cast<uint2*>(codes + da) = bad ? make_uint2(0u, 0u) : quantise8<E4M3>(x, inv, nz);
+        *reinterpret_cast<uint2*>(codes + db) = bad ? make_uint2(0u, 0u) : quantise8<E4M3>(x + 8, inv, nz);
+      } else if (at < 0 && !bad && now > old[i]) {  // an earlier row: its codes follow the scale
+        const float ratio = __fmul_rn(old[i], inv);
+        const uint4 w = *reinterpret_cast<const uint4*>(codes + 16 * u);
         const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-        float f[8], g[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          f[i] = kv8_decode<E4M3>(static_cast<uint8_t>(ww[i / 4] >> (8 * (i % 4))));
-          g[i] = kv8_decode<E4M3>(static_cast<uint8_t>(ww[2 + i / 4] >> (8 * (i % 4))));
-        }
-        const uint2 x = quantise8<E4M3>(f, ratio[j]), y = quantise8<E4M3>(g, ratio[j]);
-        *reinterpret_cast<uint4*>(p) = make_uint4(x.x, x.y, y.x, y.y);
+        for (int j = 0; j < 16; ++j) x[j] = kv8_decode<E4M3>(static_cast<uint8_t>(ww[j / 4] >> (8 * (j % 4))));
+        const uint2 y = quantise8<E4M3>(x, ratio, nz), z = quantise8<E4M3>(x + 8, ratio, nz);
+        *reinterpret_cast<uint4*>(codes + 16 * u) = make_uint4(y.x, y.y, z.x, z.y);
       }
+      if (threadIdx.x == 0) a.scales[cell] = bad ? __uint_as_float(0x7fc00000u) : now;
     }
-    __syncthreads();  // every thread has read the old scales
-    if (threadIdx.x < 2) a.scales[cell + threadIdx.x] = threadIdx.x ? now[1] : now[0];
   }
 }
 
@@ -294,14 +335,18 @@ dkv_status launch_kv8_append(const Kv8AppendArgs& a, cudaStream_t st) {
     p.rope = a.rope->table, p.rot = a.rope->rot_dim, p.max_pos = a.rope->max_pos;
     p.positions = a.rope->positions;
   }
+  p.neg_zero = -0.0f;
   p.blocks_per_seq = static_cast<int>((static_cast<int64_t>(a.max_new) + sh.block_tokens - 2) / sh.block_tokens + 1);
   const int threads = sh.block_tokens * sh.head_dim / 16;
-  p.head_steps = 1;
-  p.kv_ctas = static_cast<int64_t>(a.num_seqs) * p.blocks_per_seq * p.heads;
+  const int batch = sh.dtype == DKV_F32 ? kAppendHeads<float> : kAppendHeads<__nv_bfloat16>;
+  p.head_steps = batch;
+  const int64_t blocks = static_cast<int64_t>(a.num_seqs) * p.blocks_per_seq;
+  p.kv_ctas = blocks * ceil_div64(p.heads, p.head_steps) * 2;
   int64_t q_ctas = 0;
   if (a.q) {
-    p.q_head_steps = 4;
     const int per = threads / (sh.head_dim / 16);
+    // two batches where there are tokens enough: a thread's search for its sequence and its angles serve more heads
+    p.q_head_steps = a.total_new * p.q_heads * sh.head_dim / 16 >= int64_t{16} * 1024 * num_sms() ? 2 * batch : batch;
     q_ctas = ceil_div64(a.total_new, per) * ceil_div64(p.q_heads, p.q_head_steps);
   }
   if (p.kv_ctas + q_ctas > INT32_MAX) return DKV_ERR_UNSUPPORTED;
