@@ -52,9 +52,9 @@ static dkv_status launch_combine(const Kv8Attn& p, cudaStream_t st) {
              : DKV_ERR_CUDA;
 }
 
-template <int D, bool E4M3, int NT>
+template <int D, bool E4M3, int NT, bool BIAS>
 static dkv_status attn_stream(const Kv8Attn& p, cudaStream_t st) {
-  constexpr auto kKernel = kv8_stream_kernel<D, E4M3, NT>;
+  constexpr auto kKernel = kv8_stream_kernel<D, E4M3, NT, BIAS>;
   if (!ensure_max_dynamic_smem<kKernel, true>()) return DKV_ERR_CUDA;
   CUtensorMap map;
   if (!make_map_codes(&map, p.codes, static_cast<uint64_t>(p.num_blocks) * p.heads * 2 * p.block, D)) return DKV_ERR_CUDA;
@@ -80,12 +80,17 @@ static dkv_status attn_tile(const Kv8Attn& p, cudaStream_t st) {
   return launch_combine<__nv_bfloat16, D>(p, st);
 }
 
+template <int D, bool E4M3, bool BIAS>
+static dkv_status attn_rows(const Kv8Attn& p, cudaStream_t st) {
+  const int64_t rows = static_cast<int64_t>(p.max_q) * p.group;
+  if (rows <= 8) return attn_stream<D, E4M3, 1, BIAS>(p, st);
+  if (rows <= kStreamMaxRows) return attn_stream<D, E4M3, 2, BIAS>(p, st);
+  return attn_tile<D, E4M3, BIAS>(p, st);
+}
+
 template <int D, bool E4M3>
 static dkv_status attn_bf16(const Kv8Attn& p, cudaStream_t st) {
-  const int64_t rows = static_cast<int64_t>(p.max_q) * p.group;
-  if (rows <= 8) return attn_stream<D, E4M3, 1>(p, st);
-  if (rows <= kStreamMaxRows) return attn_stream<D, E4M3, 2>(p, st);
-  return p.softcap > 0.f || p.slopes ? attn_tile<D, E4M3, true>(p, st) : attn_tile<D, E4M3, false>(p, st);
+  return p.softcap > 0.f || p.slopes ? attn_rows<D, E4M3, true>(p, st) : attn_rows<D, E4M3, false>(p, st);
 }
 
 template <typename T, int D, bool E4M3>

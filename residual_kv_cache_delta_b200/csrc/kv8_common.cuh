@@ -134,12 +134,13 @@ __device__ __forceinline__ float kv8_decode(uint8_t c) {
   return static_cast<float>(static_cast<int8_t>(c));
 }
 
-// Score in the log2 domain.  dot: q.k of the dequantised key times the softmax scale (natural units).  With a cap,
-// cap * tanh(dot / cap) = cap - 2 cap / (1 + exp(2 dot / cap)): the hardware exp2 and a division keep the absolute
-// error near 1e-7 cap, where tanh.approx would leave 5e-4 cap.
+// cap * tanh(dot / cap) as cap - 2 cap / (1 + exp(2 dot / cap)), with the hardware's exp2 and reciprocal: an absolute error
+// near 2^-21 cap, where tanh.approx would leave 2^-11 cap.
 __device__ __forceinline__ float kv8_cap(float dot, float cap) {
-  const float e = exp2f(dot * (2.0f * kLog2e / cap));
-  return cap - 2.0f * cap / (1.0f + e);
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(dot * (2.0f * kLog2e / cap)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return fmaf(-2.0f * cap, r, cap);
 }
 
 // Merges the splits of one query row and head: out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.  Thread per

@@ -92,7 +92,8 @@ __device__ __forceinline__ void q_pairs(const uint4& w, float f, uint32_t* out) 
     out[i] = pack_f16(__uint_as_float(x[i] << 16) * f, __uint_as_float(x[i] & 0xffff0000u) * f);
 }
 
-template <int D, bool E4M3, int NT>
+// BIAS: scores may be capped or biased by distance.
+template <int D, bool E4M3, int NT, bool BIAS>
 __global__ void __launch_bounds__(kStreamWarps * 32, NT == 1 ? 2 : 1)
     kv8_stream_kernel(const __grid_constant__ CUtensorMap map, const Kv8Attn a, int row_tiles) {
   constexpr int kSteps = D / 16, kStg = stream_stages<D>(NT), kRows = 8 * NT;
@@ -137,17 +138,18 @@ __global__ void __launch_bounds__(kStreamWarps * 32, NT == 1 ? 2 : 1)
   const uint32_t bar0 = smem_u32(&bars[warp * kStg]);
   // lane i holds cell (batch * 32 + i): first row of its K codes in the tensor map (-1: no such block) and its scales
   int krow[2] = {-1, -1};
-  float ksc[2] = {0.f, 0.f}, vsc[2] = {1.f, 1.f};
-  auto load_batch = [&](int j, int& row, float& ks, float& vs) {
-    row = -1, ks = 0.f, vs = 1.f;
+  float ksc[2] = {0.f, 0.f}, vlog[2] = {0.f, 0.f}, vinv[2] = {1.f, 1.f};  // K scale, log2 and inverse of the V scale
+  auto load_batch = [&](int j, int& row, float& ks, float& lv, float& iv) {
+    row = -1, ks = 0.f, lv = 0.f, iv = 1.f;
     if (j >= n) return;
     const int key = span.cell(v0 + warp + j * kStreamWarps) * kKv8CellKeys;
     const int blk = kv8_block(a.block_tables, a.max_blocks, a.num_blocks, s, key / a.block);
     if (blk < 0) return;
     const int cell = (blk * a.heads + h) * 2;
     const float2 sc = *reinterpret_cast<const float2*>(a.scales + cell);
+    const float vs = sc.y < kLeastScale ? kLeastScale : sc.y;  // a zero scale has no logarithm; NaN stays
     row = cell * a.block + key % a.block;
-    ks = sc.x, vs = sc.y;
+    ks = BIAS ? sc.x : sc.x * kLog2e, lv = __log2f(vs), iv = __frcp_rn(vs);
   };
   auto issue = [&](int j, int row) {  // lane 0
     const uint32_t bar = bar0 + (j % kStg) * 8, dst = ring + (j % kStg) * kCellBytes;
@@ -159,7 +161,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, NT == 1 ? 2 : 1)
     tma_load_2d(dst, &map, 0, row, bar);
     tma_load_2d(dst + kCellBytes / 2, &map, 0, row + a.block, bar);
   };
-  load_batch(lane, krow[0], ksc[0], vsc[0]);
+  load_batch(lane, krow[0], ksc[0], vlog[0], vinv[0]);
 #pragma unroll
   for (int j = 0; j < kStg; ++j) {
     const int row = __shfl_sync(~0u, krow[0], j);
@@ -207,6 +209,14 @@ __global__ void __launch_bounds__(kStreamWarps * 32, NT == 1 ? 2 : 1)
     }
   }
 
+  int all_lo = 0, all_hi = INT_MAX;  // keys that every row sees
+#pragma unroll
+  for (int c = 0; c < NT; ++c)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) all_lo = max(all_lo, row[c][j].lo), all_hi = min(all_hi, row[c][j].hi);
+  all_lo = __reduce_max_sync(~0u, all_lo);
+  all_hi = __reduce_min_sync(~0u, all_hi);
+
   float m[NT][2], l[NT][2], o[NT][kSteps][4];
 #pragma unroll
   for (int c = 0; c < NT; ++c) {
@@ -227,22 +237,21 @@ __global__ void __launch_bounds__(kStreamWarps * 32, NT == 1 ? 2 : 1)
   bool alive = true;
   for (int j = 0; j < n; ++j) {
     if ((j & 31) == 0) {
-      if (j > 0) krow[0] = krow[1], ksc[0] = ksc[1], vsc[0] = vsc[1];
-      load_batch(j + 32 + lane, krow[1], ksc[1], vsc[1]);
+      if (j > 0) krow[0] = krow[1], ksc[0] = ksc[1], vlog[0] = vlog[1], vinv[0] = vinv[1];
+      load_batch(j + 32 + lane, krow[1], ksc[1], vlog[1], vinv[1]);
     }
     const int ahead = (j & 31) + kStg;  // cell j + kStg lies in this batch or the next
     const int next_row = __shfl_sync(~0u, ahead < 32 ? krow[0] : krow[1], ahead & 31);
     const bool there = __shfl_sync(~0u, krow[0], j & 31) >= 0;
     const float ks = __shfl_sync(~0u, ksc[0], j & 31);
-    float vs = __shfl_sync(~0u, vsc[0], j & 31);
-    if (vs < kLeastScale) vs = kLeastScale;  // a zero scale has no logarithm; NaN stays
+    const float lv = __shfl_sync(~0u, vlog[0], j & 31), iv = __shfl_sync(~0u, vinv[0], j & 31);
     alive = __all_sync(~0u, mbar_wait(bar0 + stage * 8, phase, &abort_flag));
     if (!alive) break;
     if (there) {
       const uint8_t* kbuf = smem + (warp * kStg + stage) * kCellBytes;
       const uint8_t* vbuf = kbuf + kCellBytes / 2;
       const int key0 = span.cell(v0 + warp + j * kStreamWarps) * kKv8CellKeys;
-      const float lv = __log2f(vs), iv = __frcp_rn(vs);
+      const bool whole = key0 >= all_lo && key0 + kKv8CellKeys <= all_hi + 1;  // every row sees every key
       // scores
       uint32_t kw[2][D / 16];
 #pragma unroll
@@ -266,22 +275,32 @@ __global__ void __launch_bounds__(kStreamWarps * 32, NT == 1 ? 2 : 1)
         for (int c = 0; c < NT; ++c) mma_f16_16816(sc[c][i & 1], f, qf[c][2 * i], qf[c][2 * i + 1]);
       }
       // weights; element i: key kg + 8 (i / 2), column 2t + i % 2
-      const bool whole = key0 + kKv8CellKeys <= seq.T;
       uint32_t pf[NT][2];
 #pragma unroll
       for (int c = 0; c < NT; ++c) {
         float z[4];
         bool over = false;
+        const float kk[2] = {ks * scl[c][0], ks * scl[c][1]};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int key = key0 + kg + 8 * (i >> 1);
-          float x = (sc[c][0][i] + sc[c][1][i]) * (ks * scl[c][i & 1]);
-          if (a.softcap > 0.f) x = kv8_cap(x, a.softcap);
-          x = fmaf(x, kLog2e, lv) - slope[c][i & 1] * static_cast<float>(abs(row[c][i & 1].pos - key));
-          if (!kv8_sees(row[c][i & 1], seq.prefix, key)) x = -INFINITY;
+          float x = sc[c][0][i] + sc[c][1][i];
+          if (BIAS) {
+            x *= kk[i & 1];
+            if (a.softcap > 0.f) x = kv8_cap(x, a.softcap);
+            x = fmaf(x, kLog2e, lv) -
+                slope[c][i & 1] * static_cast<float>(abs(row[c][i & 1].pos - key0 - kg - 8 * (i >> 1)));
+          } else {
+            x = fmaf(x, kk[i & 1], lv);
+          }
           z[i] = x;
-          over |= x > m[c][i & 1] + kMaxSlack;
         }
+        if (!whole) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (!kv8_sees(row[c][i & 1], seq.prefix, key0 + kg + 8 * (i >> 1))) z[i] = -INFINITY;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) over |= z[i] > m[c][i & 1] + kMaxSlack;
         if (__any_sync(~0u, over)) {  // some column's maximum rises: all lanes of a column take the same new one
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
@@ -297,10 +316,12 @@ __global__ void __launch_bounds__(kStreamWarps * 32, NT == 1 ? 2 : 1)
           }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          z[i] = fast_exp2(z[i] - m[c][i & 1]);
+        for (int i = 0; i < 4; ++i) z[i] = fast_exp2(z[i] - m[c][i & 1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
           // a key out of sight adds nothing, even where its block's scale is NaN
-          if (z[i] != 0.f) l[c][i & 1] = fmaf(z[i], iv, l[c][i & 1]);
+          const float sum = z[e] + z[2 + e];
+          if (whole || sum != 0.f) l[c][e] = fmaf(sum, iv, l[c][e]);
         }
         pf[c][0] = movmatrix_t(pack_f16(z[0], z[1]));
         pf[c][1] = movmatrix_t(pack_f16(z[2], z[3]));
@@ -316,12 +337,16 @@ __global__ void __launch_bounds__(kStreamWarps * 32, NT == 1 ? 2 : 1)
           const uint2 x = *reinterpret_cast<const uint2*>(vbuf + stream_chunk<D>(kt[r], g >> 1) + (g & 1) * 8);
           vw[r][0] = x.x, vw[r][1] = x.y;
         }
-        // rows behind the context's end hold anything, e4m3 NaN codes too: weight 0 times them must stay 0
-        if (!whole && key0 + kt[r] >= seq.T)
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) vw[r][i] = 0;
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) vw[r][i] = flip_sign<E4M3>(vw[r][i]);
+      }
+      if (!whole && key0 + kKv8CellKeys > seq.T) {
+        // rows behind the context's end hold anything, e4m3 NaN codes too: weight 0 times them must stay 0
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (key0 + kt[r] >= seq.T)
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) vw[r][i] = 0;
       }
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
