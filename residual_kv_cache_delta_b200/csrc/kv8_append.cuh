@@ -1,7 +1,7 @@
 // Append to the 8-bit paged cache: position rotation of K (and q), quantisation, paged write.
 //
 // Bound by memory: every input value is read once and every code written once.  A CTA owns K or V of one block of one
-// sequence and walks kv heads; a thread owns 16 dimensions of one row ("unit"), so that a block's largest magnitude is a
+// sequence for a few kv heads; a thread owns 16 dimensions of one row ("unit"), so that a block's largest magnitude is a
 // reduction over registers, and loads several heads at once, before anything that it does not need for their addresses.
 // Unit u of a rotated row holds dimensions whose partners it also holds: 8u .. 8u+7 of the first half and of the second
 // (halves), or 16u .. 16u+15 (pairs); both use entries 8u .. 8u+7 of the cosines and sines, which stay in registers.
@@ -32,7 +32,6 @@ struct Kv8Append {
   int rot, max_pos;
   const int* positions;
   int blocks_per_seq;  // blocks that max_new tokens can touch
-  int head_steps;      // kv heads a CTA walks
   int64_t kv_ctas;
   int q_head_steps;    // q heads a thread walks
   float neg_zero;      // -0, not known to the compiler
@@ -49,6 +48,9 @@ struct Oct<float> {
   }
   static __device__ __forceinline__ Oct make(const float* f) {
     return {make_float4(f[0], f[1], f[2], f[3]), make_float4(f[4], f[5], f[6], f[7])};
+  }
+  __device__ __forceinline__ void forget() {
+    asm volatile("" : "+f"(v.x), "+f"(v.y), "+f"(v.z), "+f"(v.w), "+f"(w.x), "+f"(w.y), "+f"(w.z), "+f"(w.w));
   }
 };
 template <>
@@ -68,6 +70,8 @@ struct Oct<__nv_bfloat16> {
     }
     return {make_uint4(w[0], w[1], w[2], w[3])};
   }
+  // Makes the compiler take the value for a new one, so that what was computed from it before is not kept in registers.
+  __device__ __forceinline__ void forget() { asm volatile("" : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w)); }
 };
 template <typename T>
 struct Unit {
@@ -209,6 +213,7 @@ __device__ __forceinline__ void append_q(const Kv8Append& a, int64_t cta) {
   float cs[16], x[16];
   const uint64_t nz = pack2(a.neg_zero, a.neg_zero);
   const bool turn = load_angles(a, pos, u, cs);
+#pragma unroll 1
   for (int h = h0; h < h1; h += kN) {
     if (h > h0) load_heads<T, D>(src, h, h1, da, db, true, raw);
 #pragma unroll
@@ -223,19 +228,19 @@ __device__ __forceinline__ void append_q(const Kv8Append& a, int64_t cta) {
 }
 
 template <typename T, int D, bool E4M3, bool PAIRS>
-__global__ void __maxnreg__(72) kv8_append_kernel(const __grid_constant__ Kv8Append a) {
+__global__ void __maxnreg__(80) kv8_append_kernel(const __grid_constant__ Kv8Append a) {
   constexpr int kUnits = D / 16, kN = kAppendHeads<T>;
   constexpr float kTop = E4M3 ? 448.0f : 127.0f;
-  __shared__ uint32_t tops[2][kN][16];
+  __shared__ uint32_t tops[kN][16];
   if (blockIdx.x >= a.kv_ctas) {
     append_q<T, D, PAIRS>(a, blockIdx.x - a.kv_ctas);
     return;
   }
-  const int steps = (a.heads + a.head_steps - 1) / a.head_steps;
+  const int steps = (a.heads + kN - 1) / kN;
   int64_t id = blockIdx.x;
   const int half = static_cast<int>(id & 1);  // 0: K, 1: V
   id >>= 1;
-  const int h0 = static_cast<int>(id % steps) * a.head_steps, h1 = min(h0 + a.head_steps, a.heads);
+  const int h0 = static_cast<int>(id % steps) * kN, h1 = min(h0 + kN, a.heads);
   id /= steps;
   const int nth = static_cast<int>(id % a.blocks_per_seq), s = static_cast<int>(id / a.blocks_per_seq);
   const int row0 = a.cu_new[s], n = a.cu_new[s + 1] - row0, start = a.start_pos[s];
@@ -264,50 +269,47 @@ __global__ void __maxnreg__(72) kv8_append_kernel(const __grid_constant__ Kv8App
   bool turn = false;
   if (half == 0 && fresh && a.rot > 0) turn = load_angles(a, a.positions ? a.positions[tok] : start + at, u, cs);
   const int warps = blockDim.x / 32, warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  int slot = 0;
-  for (int h = h0; h < h1; h += kN, slot ^= 1) {
-    if (h > h0) load_heads<T, D>(src, h, h1, da, db, fresh, raw);
-    float x[16], old[kN];
+  float x[16], old[kN];
 #pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      old[i] = 0.f;
-      if (held && h + i < h1) old[i] = a.scales[(static_cast<int64_t>(blk) * a.heads + h + i) * 2 + half];
+  for (int i = 0; i < kN; ++i) {
+    old[i] = 0.f;
+    if (held && h0 + i < h1) old[i] = a.scales[(static_cast<int64_t>(blk) * a.heads + h0 + i) * 2 + half];
+    raw[i].a.get(x), raw[i].b.get(x + 8);
+    if (turn) rotate_unit<PAIRS>(x, cs, nz);
+    float top = fabsf(x[0]);
+#pragma unroll
+    for (int j = 1; j < 16; ++j) top = max_nan(top, fabsf(x[j]));
+    // bit patterns of magnitudes order like the magnitudes, with infinities and then NaN on top
+    const uint32_t m = __reduce_max_sync(~0u, __float_as_uint(top) & 0x7fffffffu);
+    if (lane == 0) tops[i][warp] = m;
+  }
+  __syncthreads();  // also: every thread has read the old scales
+#pragma unroll
+  for (int i = 0; i < kN; ++i) {
+    if (h0 + i >= h1) continue;
+    const uint32_t m = __reduce_max_sync(~0u, lane < warps ? tops[i][lane] : 0u);
+    const int64_t cell = (static_cast<int64_t>(blk) * a.heads + h0 + i) * 2 + half;
+    const float now = fmaxf(fmaxf(__uint_as_float(m), kKv8Floor) * (1.0f / kTop), old[i]);
+    // a value is not finite: the block reads as NaN from here on
+    const bool bad = m >= 0x7f800000u || !(fabsf(old[i]) <= 3.402823466e38f);
+    const float inv = __frcp_rn(now);
+    uint8_t* codes = a.codes + (cell * a.block + r) * D;
+    if (fresh) {  // rotated once more: cheaper than to keep the fp32 values of four heads
+      raw[i].a.forget(), raw[i].b.forget();
       raw[i].a.get(x), raw[i].b.get(x + 8);
       if (turn) rotate_unit<PAIRS>(x, cs, nz);
-      float top = fabsf(x[0]);
+      *reinterpret_cast<uint2*>(codes + da) = bad ? make_uint2(0u, 0u) : quantise8<E4M3>(x, inv, nz);
+      *reinterpret_cast<uint2*>(codes + db) = bad ? make_uint2(0u, 0u) : quantise8<E4M3>(x + 8, inv, nz);
+    } else if (at < 0 && !bad && now > old[i]) {  // an earlier row: its codes follow the scale
+      const float ratio = __fmul_rn(old[i], inv);
+      const uint4 w = *reinterpret_cast<const uint4*>(codes + 16 * u);
+      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-      for (int j = 1; j < 16; ++j) top = max_nan(top, fabsf(x[j]));
-      // bit patterns of magnitudes order like the magnitudes, with infinities and then NaN on top
-      const uint32_t m = __reduce_max_sync(~0u, __float_as_uint(top) & 0x7fffffffu);
-      if (lane == 0) tops[slot][i][warp] = m;
+      for (int j = 0; j < 16; ++j) x[j] = kv8_decode<E4M3>(static_cast<uint8_t>(ww[j / 4] >> (8 * (j % 4))));
+      const uint2 y = quantise8<E4M3>(x, ratio, nz), z = quantise8<E4M3>(x + 8, ratio, nz);
+      *reinterpret_cast<uint4*>(codes + 16 * u) = make_uint4(y.x, y.y, z.x, z.y);
     }
-    __syncthreads();  // also: every thread has read the old scales
-#pragma unroll
-    for (int i = 0; i < kN; ++i) {
-      if (h + i >= h1) continue;
-      const uint32_t m = __reduce_max_sync(~0u, lane < warps ? tops[slot][i][lane] : 0u);
-      const int64_t cell = (static_cast<int64_t>(blk) * a.heads + h + i) * 2 + half;
-      const float now = fmaxf(fmaxf(__uint_as_float(m), kKv8Floor) * (1.0f / kTop), old[i]);
-      // a value is not finite: the block reads as NaN from here on
-      const bool bad = m >= 0x7f800000u || !(fabsf(old[i]) <= 3.402823466e38f);
-      const float inv = __frcp_rn(now);
-      uint8_t* codes = a.codes + (cell * a.block + r) * D;
-      if (fresh) {  // rotated once more: cheaper than to keep the fp32 values of four heads
-        raw[i].a.get(x), raw[i].b.get(x + 8);
-        if (turn) rotate_unit<PAIRS>(x, cs, nz);
-        *reinterpret_cast<uint2*>(codes + da) = bad ? make_uint2(0u, 0u) : quantise8<E4M3>(x, inv, nz);
-        *reinterpret_cast<uint2*>(codes + db) = bad ? make_uint2(0u, 0u) : quantise8<E4M3>(x + 8, inv, nz);
-      } else if (at < 0 && !bad && now > old[i]) {  // an earlier row: its codes follow the scale
-        const float ratio = __fmul_rn(old[i], inv);
-        const uint4 w = *reinterpret_cast<const uint4*>(codes + 16 * u);
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int j = 0; j < 16; ++j) x[j] = kv8_decode<E4M3>(static_cast<uint8_t>(ww[j / 4] >> (8 * (j % 4))));
-        const uint2 y = quantise8<E4M3>(x, ratio, nz), z = quantise8<E4M3>(x + 8, ratio, nz);
-        *reinterpret_cast<uint4*>(codes + 16 * u) = make_uint4(y.x, y.y, z.x, z.y);
-      }
-      if (threadIdx.x == 0) a.scales[cell] = bad ? __uint_as_float(0x7fc00000u) : now;
-    }
+    if (threadIdx.x == 0) a.scales[cell] = bad ? __uint_as_float(0x7fc00000u) : now;
   }
 }
 
@@ -339,9 +341,8 @@ dkv_status launch_kv8_append(const Kv8AppendArgs& a, cudaStream_t st) {
   p.blocks_per_seq = static_cast<int>((static_cast<int64_t>(a.max_new) + sh.block_tokens - 2) / sh.block_tokens + 1);
   const int threads = sh.block_tokens * sh.head_dim / 16;
   const int batch = sh.dtype == DKV_F32 ? kAppendHeads<float> : kAppendHeads<__nv_bfloat16>;
-  p.head_steps = batch;
   const int64_t blocks = static_cast<int64_t>(a.num_seqs) * p.blocks_per_seq;
-  p.kv_ctas = blocks * ceil_div64(p.heads, p.head_steps) * 2;
+  p.kv_ctas = blocks * ceil_div64(p.heads, batch) * 2;
   int64_t q_ctas = 0;
   if (a.q) {
     const int per = threads / (sh.head_dim / 16);

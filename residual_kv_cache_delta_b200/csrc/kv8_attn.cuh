@@ -9,29 +9,32 @@ namespace dkv {
 // Up to so many rows per kv head the streaming kernel is taken, above it the tcgen05 one.
 constexpr int kStreamMaxRows = 16;
 
-// How many query rows a CTA takes, how many CTAs the device holds at once, and how many key ranges a row is cut into.
+// How many query rows a CTA takes and how many key ranges a row is cut into.
 struct Kv8Plan {
-  int tile, slots, nsplit;
+  int tile, nsplit;
 };
 
-static Kv8Plan kv8_plan(const dkv_kv8_shape& sh, int num_seqs, int max_q, int max_ctx) {
+// span: most keys that a query token sees.
+static Kv8Plan kv8_plan(const dkv_kv8_shape& sh, int num_seqs, int max_q, int span) {
   const int64_t rows = static_cast<int64_t>(max_q) * (sh.num_q_heads / sh.num_kv_heads);
   Kv8Plan p;
-  if (sh.dtype == DKV_F32)
-    p.tile = kSimpleRows, p.slots = 4 * num_sms();
-  else if (rows <= kStreamMaxRows)
-    p.tile = rows <= 8 ? 8 : 16, p.slots = num_sms() * (rows <= 8 ? 2 : 1);
-  else
-    p.tile = kTileRows, p.slots = num_sms();
+  const bool tiles = sh.dtype != DKV_F32 && rows > kStreamMaxRows;
+  p.tile = sh.dtype == DKV_F32 ? kSimpleRows : tiles ? kTileRows : rows <= 8 ? 8 : 16;
+  const int per_sm = sh.dtype == DKV_F32 ? 4 : p.tile == 8 ? 2 : 1;
   const int64_t base = ceil_div64(rows, p.tile) * sh.num_kv_heads * std::max(num_seqs, 1);
-  const int64_t cells = ceil_div64(max_ctx, kKv8CellKeys);
+  const int64_t cells = ceil_div64(span, kKv8CellKeys);
+  const int64_t sms = num_sms();
   const int most = static_cast<int>(std::max<int64_t>(
       1, std::min<int64_t>(kKv8MaxSplits, ceil_div64(cells, kKv8MinSplitCells))));
-  // waves of CTAs times the length of one, counted in cells; a CTA's start and end cost about as much as 32 cells
+  // Time in cells of one SM: the fullest SM's share of the cells, a start and an end for each of its rounds of CTAs, and
+  // with splits the join (tcgen05 kernel: 256 rows of fp32 written and read again per CTA).
   p.nsplit = 1;
   double best = 0;
   for (int n = 1; n <= most; ++n) {
-    const double t = static_cast<double>(ceil_div64(base * n, p.slots)) * (static_cast<double>(cells) / n + 32.0);
+    const int64_t ctas = base * n;
+    double t = static_cast<double>(ceil_div64(ctas, sms)) * (static_cast<double>(cells) / n) +
+               24.0 * static_cast<double>(ceil_div64(ctas, sms * per_sm));
+    if (n > 1) t += 20.0 + (tiles ? 40.0 * static_cast<double>(ceil_div64(ctas, sms)) : 0.0);
     if (n == 1 || t < best) best = t, p.nsplit = n;
   }
   return p;
@@ -41,15 +44,17 @@ int kv8_attn_splits(const dkv_kv8_shape& sh, int num_seqs, int64_t total_q, int 
   return kv8_plan(sh, num_seqs, max_q, max_ctx).nsplit;
 }
 
-// Joins the splits of each row; starts while the attention kernel's last CTAs run.
+// Joins the splits of each row; starts while the attention kernel's last CTAs run.  With more than 8 splits four warps share
+// a row.
 template <typename T, int D>
 static dkv_status launch_combine(const Kv8Attn& p, cudaStream_t st) {
   if (p.nsplit == 1) return DKV_OK;
   const int64_t rows = p.total_q * p.heads * p.group;
-  return launch_programmatic(kv8_combine_kernel<T, D>, dim3(static_cast<unsigned>(ceil_div64(rows, 512 / D))),
-                             dim3(128), 0, st, p) == cudaSuccess
-             ? DKV_OK
-             : DKV_ERR_CUDA;
+  const cudaError_t e =
+      p.nsplit > 8 ? launch_programmatic(kv8_combine_kernel<T, D, 4>, dim3(static_cast<unsigned>(rows)), dim3(128), 0, st, p)
+                   : launch_programmatic(kv8_combine_kernel<T, D, 1>, dim3(static_cast<unsigned>(ceil_div64(rows, 4))),
+                                         dim3(128), 0, st, p);
+  return e == cudaSuccess ? DKV_OK : DKV_ERR_CUDA;
 }
 
 template <int D, bool E4M3, int NT, bool BIAS>
@@ -119,6 +124,9 @@ dkv_status launch_kv8_attention(const Kv8AttnArgs& a, const Kv8AttnWs& w, void* 
     p.prefix_lens = a.score->prefix_lens, p.first_key = a.score->first_key;
   }
   p.out = a.out, p.lse = a.lse, p.nsplit = w.nsplit;
+  if (p.window > 0 && p.window < a.max_ctx)  // fewer keys to share out than the workspace was sized for
+    p.nsplit = std::min(p.nsplit, kv8_plan(sh, a.num_seqs, a.max_q, static_cast<int>(std::min<int64_t>(
+                                               a.max_ctx, int64_t{a.max_q} + p.window))).nsplit);
   p.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + w.ml);
   p.o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.o);
   const bool e4 = sh.code == DKV_KV8_E4M3, d64 = sh.head_dim == 64;

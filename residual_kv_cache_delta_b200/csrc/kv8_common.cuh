@@ -136,51 +136,89 @@ __device__ __forceinline__ float kv8_decode(uint8_t c) {
 
 // cap * tanh(dot / cap) as cap - 2 cap / (1 + exp(2 dot / cap)), with the hardware's exp2 and reciprocal: an absolute error
 // near 2^-21 cap, where tanh.approx would leave 2^-11 cap.
-__device__ __forceinline__ float kv8_cap(float dot, float cap) {
+// two_over_cap: 2 log2(e) / cap.
+__device__ __forceinline__ float kv8_cap(float dot, float cap, float two_over_cap) {
   float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(dot * (2.0f * kLog2e / cap)));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(dot * two_over_cap));
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
   return fmaf(-2.0f * cap, r, cap);
 }
 
-// Merges the splits of one query row and head: out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.  Thread per
-// 4 output values.  T: out type.
-template <typename T, int D>
-__global__ void __launch_bounds__(128) kv8_combine_kernel(const Kv8Attn a) {
-  constexpr int kVec = D / 4, kRows = 128 / kVec;
-  griddep_wait();
-  const int hq = a.heads * a.group;
-  const int64_t row = static_cast<int64_t>(blockIdx.x) * kRows + threadIdx.x / kVec;
-  const int64_t rows = a.total_q * hq;
-  if (row >= rows) return;
-  if (a.cu_q) {  // rows outside every sequence stay as they were
-    const int64_t tok = row / hq;
-    int lo = 0, hi = a.num_seqs;  // the last sequence that begins at or before tok
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (a.cu_q[mid] <= tok) lo = mid; else hi = mid;
+// Merges the splits of a query row and head: out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.  WPR warps work on a row: a
+// lane weighs split `lane` (and + 32, ...), then the warps go through the splits' rows, several loads in flight.
+// T: out type.
+template <typename T, int D, int WPR>
+__global__ void __launch_bounds__(128) kv8_combine_kernel(const __grid_constant__ Kv8Attn a) {
+  constexpr int kRows = 4 / WPR, kVec = D / 32;  // rows of a CTA; values of a lane
+  __shared__ float part[4][D];
+  const int hq = a.heads * a.group, warp = warp_id(), lane = lane_id(), sub = warp % WPR;
+  const int64_t rows = a.total_q * hq, row = static_cast<int64_t>(blockIdx.x) * kRows + warp / WPR;
+  bool on = row < rows;
+  if (on) {
+    int s = static_cast<int>(row / hq);
+    if (a.cu_q) {  // rows outside every sequence stay as they were
+      const int tok = s;
+      int lo = 0, hi = a.num_seqs;  // the last sequence that begins at or before tok
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (a.cu_q[mid] <= tok) lo = mid; else hi = mid;
+      }
+      s = lo;
+      on = tok >= a.cu_q[lo] && tok < a.cu_q[lo + 1];
     }
-    if (tok < a.cu_q[lo] || tok >= a.cu_q[lo + 1] || !kv8_seq(a, lo).ok) return;
-  } else if (!kv8_seq(a, static_cast<int>(row / hq)).ok) {
-    return;
+    if (on) on = kv8_seq(a, s).ok;
   }
-  const int c = (threadIdx.x % kVec) * 4;
-  float M = kNoMax;
-  for (int i = 0; i < a.nsplit; ++i) M = fmaxf(M, a.ml[i * rows + row].x);
-  float l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int i = 0; i < a.nsplit; ++i) {
-    const float2 p = a.ml[i * rows + row];
-    if (p.y == 0.f) continue;  // nothing seen there (a NaN sum goes on)
-    const float w = exp2f(p.x - M);
-    const float4 o = *reinterpret_cast<const float4*>(a.o + (i * rows + row) * D + c);
-    l += w * p.y;
-    acc[0] += w * o.x, acc[1] += w * o.y, acc[2] += w * o.z, acc[3] += w * o.w;
-  }
-  const float inv = l == 0.f ? 0.f : 1.0f / l;
-  T* out = static_cast<T*>(a.out) + row * D + c;
+  griddep_wait();
+  float M = kNoMax, l = 0.f, acc[kVec] = {};
+  if (on) {
+    float2 p[kKv8MaxSplits / 32];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) out[j] = Elem<T>::from_f(acc[j] * inv);
-  if (c == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
+    for (int b = 0; b < kKv8MaxSplits / 32; ++b) {
+      const int i = 32 * b + lane;
+      p[b] = i < a.nsplit ? a.ml[i * rows + row] : make_float2(kNoMax, 0.f);
+      M = fmaxf(M, p[b].x);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
+#pragma unroll
+    for (int b = 0; b < kKv8MaxSplits / 32; ++b) {
+      if (32 * b >= a.nsplit) break;
+      const float w = p[b].y == 0.f ? 0.f : exp2f(p[b].x - M);  // 0: nothing seen there (a NaN sum goes on)
+      l += w * p[b].y;
+      const int top = min(32, a.nsplit - 32 * b);
+#pragma unroll 8
+      for (int i = sub; i < top; i += WPR) {
+        const float wi = __shfl_sync(~0u, w, i);
+        if (wi == 0.f) continue;
+        const float* o = a.o + ((32 * b + i) * rows + row) * D + lane * kVec;
+        if constexpr (kVec == 4) {
+          const float4 x = *reinterpret_cast<const float4*>(o);
+          acc[0] += wi * x.x, acc[1] += wi * x.y, acc[2] += wi * x.z, acc[3] += wi * x.w;
+        } else {
+          const float2 x = *reinterpret_cast<const float2*>(o);
+          acc[0] += wi * x.x, acc[1] += wi * x.y;
+        }
+      }
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
+  }
+  if constexpr (WPR > 1) {
+#pragma unroll
+    for (int j = 0; j < kVec; ++j) part[warp][lane * kVec + j] = acc[j];
+    __syncthreads();
+    if (sub != 0) return;
+#pragma unroll
+    for (int w = 1; w < WPR; ++w)
+#pragma unroll
+      for (int j = 0; j < kVec; ++j) acc[j] += part[warp + w][lane * kVec + j];
+  }
+  if (!on) return;
+  const float inv = l == 0.f ? 0.f : 1.0f / l;
+  T* out = static_cast<T*>(a.out) + row * D + lane * kVec;
+#pragma unroll
+  for (int j = 0; j < kVec; ++j) out[j] = Elem<T>::from_f(acc[j] * inv);
+  if (lane == 0 && a.lse) a.lse[row] = l == 0.f ? -INFINITY : (M + log2f(l)) * kLn2;
 }
 
 }  // namespace dkv

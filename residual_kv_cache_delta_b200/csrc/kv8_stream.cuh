@@ -132,23 +132,43 @@ __global__ void __launch_bounds__(kStreamWarps * 32, NT == 1 ? 2 : 1)
   }
   __syncthreads();
 
-  // cells v0 + warp, v0 + warp + W, ...: this warp's j-th
+  // q rows of the columns, on their way while the first block ids are
+  uint4 qw[NT][D / 32];
+#pragma unroll
+  for (int c = 0; c < NT; ++c) {
+    const int r = r0 + c * 8 + g;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) qw[c][i] = make_uint4(0u, 0u, 0u, 0u);
+    if (r < r1) {
+      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) +
+                                 (seq.q0 + r / a.group) * a.q_stride + (h * a.group + r % a.group) * D;
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        qw[c][2 * i] = *reinterpret_cast<const uint4*>(src + 64 * i + 16 * t);
+        qw[c][2 * i + 1] = *reinterpret_cast<const uint4*>(src + 64 * i + 16 * t + 8);
+      }
+    }
+  }
+
+  // This warp's j-th cell is v1 - 1 - warp - W j: from the nearest keys to the farthest, so that a distance bias does not
+  // raise the running maximum at every cell
   const int n = v1 - v0 > warp ? (v1 - v0 - warp + kStreamWarps - 1) / kStreamWarps : 0;
   const uint32_t ring = smem_u32(smem) + warp * kStg * kCellBytes;
   const uint32_t bar0 = smem_u32(&bars[warp * kStg]);
-  // lane i holds cell (batch * 32 + i): first row of its K codes in the tensor map (-1: no such block) and its scales
+  // lane i holds cell (batch * 32 + i): first row of its K codes in the tensor map (-1: no such block), its K scale, and
+  // log2 and inverse of its V scale
   int krow[2] = {-1, -1};
-  float ksc[2] = {0.f, 0.f}, vlog[2] = {0.f, 0.f}, vinv[2] = {1.f, 1.f};  // K scale, log2 and inverse of the V scale
-  auto load_batch = [&](int j, int& row, float& ks, float& lv, float& iv) {
-    row = -1, ks = 0.f, lv = 0.f, iv = 1.f;
-    if (j >= n) return;
-    const int key = span.cell(v0 + warp + j * kStreamWarps) * kKv8CellKeys;
-    const int blk = kv8_block(a.block_tables, a.max_blocks, a.num_blocks, s, key / a.block);
-    if (blk < 0) return;
-    const int cell = (blk * a.heads + h) * 2;
-    const float2 sc = *reinterpret_cast<const float2*>(a.scales + cell);
+  float ksc[2] = {0.f, 0.f}, vlog[2] = {0.f, 0.f}, vinv[2] = {1.f, 1.f};
+  auto first_key = [&](int j) { return span.cell(v1 - 1 - warp - j * kStreamWarps) * kKv8CellKeys; };
+  auto load_row = [&](int j) {
+    if (j >= n) return -1;
+    const int key = first_key(j), blk = kv8_block(a.block_tables, a.max_blocks, a.num_blocks, s, key / a.block);
+    return blk < 0 ? -1 : (blk * a.heads + h) * 2 * a.block + key % a.block;
+  };
+  auto load_scales = [&](int row, float& ks, float& lv, float& iv) {
+    float2 sc = make_float2(0.f, 1.f);
+    if (row >= 0) sc = *reinterpret_cast<const float2*>(a.scales + row / (2 * a.block) * 2);
     const float vs = sc.y < kLeastScale ? kLeastScale : sc.y;  // a zero scale has no logarithm; NaN stays
-    row = cell * a.block + key % a.block;
     ks = BIAS ? sc.x : sc.x * kLog2e, lv = __log2f(vs), iv = __frcp_rn(vs);
   };
   auto issue = [&](int j, int row) {  // lane 0
@@ -161,12 +181,13 @@ __global__ void __launch_bounds__(kStreamWarps * 32, NT == 1 ? 2 : 1)
     tma_load_2d(dst, &map, 0, row, bar);
     tma_load_2d(dst + kCellBytes / 2, &map, 0, row + a.block, bar);
   };
-  load_batch(lane, krow[0], ksc[0], vlog[0], vinv[0]);
+  krow[0] = load_row(lane);
 #pragma unroll
   for (int j = 0; j < kStg; ++j) {
     const int row = __shfl_sync(~0u, krow[0], j);
     if (lane == 0 && j < n) issue(j, row);
   }
+  load_scales(krow[0], ksc[0], vlog[0], vinv[0]);
 
   // q fragments and the columns' parameters
   uint32_t qf[NT][2 * kSteps];
@@ -174,17 +195,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, NT == 1 ? 2 : 1)
   Kv8Row row[NT][2];
 #pragma unroll
   for (int c = 0; c < NT; ++c) {
-    const int r = r0 + c * 8 + g;
-    uint4 w[D / 32] = {};
-    if (r < r1) {
-      const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) +
-                                 (seq.q0 + r / a.group) * a.q_stride + (h * a.group + r % a.group) * D;
-#pragma unroll
-      for (int i = 0; i < D / 64; ++i) {
-        w[2 * i] = *reinterpret_cast<const uint4*>(src + 64 * i + 16 * t);
-        w[2 * i + 1] = *reinterpret_cast<const uint4*>(src + 64 * i + 16 * t + 8);
-      }
-    }
+    const uint4(&w)[D / 32] = qw[c];
     uint32_t top = 0;  // largest magnitude of the row, as bits
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
@@ -227,6 +238,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, NT == 1 ? 2 : 1)
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[c][i][j] = 0.f;
   }
+  const float two_over_cap = BIAS && a.softcap > 0.f ? 2.0f * kLog2e / a.softcap : 0.f;
   const int kg = stream_perm<D>(g);
   int kt[4];  // keys whose V a lane reads
 #pragma unroll
@@ -238,7 +250,8 @@ __global__ void __launch_bounds__(kStreamWarps * 32, NT == 1 ? 2 : 1)
   for (int j = 0; j < n; ++j) {
     if ((j & 31) == 0) {
       if (j > 0) krow[0] = krow[1], ksc[0] = ksc[1], vlog[0] = vlog[1], vinv[0] = vinv[1];
-      load_batch(j + 32 + lane, krow[1], ksc[1], vlog[1], vinv[1]);
+      krow[1] = load_row(j + 32 + lane);
+      load_scales(krow[1], ksc[1], vlog[1], vinv[1]);
     }
     const int ahead = (j & 31) + kStg;  // cell j + kStg lies in this batch or the next
     const int next_row = __shfl_sync(~0u, ahead < 32 ? krow[0] : krow[1], ahead & 31);
@@ -250,7 +263,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, NT == 1 ? 2 : 1)
     if (there) {
       const uint8_t* kbuf = smem + (warp * kStg + stage) * kCellBytes;
       const uint8_t* vbuf = kbuf + kCellBytes / 2;
-      const int key0 = span.cell(v0 + warp + j * kStreamWarps) * kKv8CellKeys;
+      const int key0 = first_key(j);
       const bool whole = key0 >= all_lo && key0 + kKv8CellKeys <= all_hi + 1;  // every row sees every key
       // scores
       uint32_t kw[2][D / 16];
@@ -283,16 +296,21 @@ __global__ void __launch_bounds__(kStreamWarps * 32, NT == 1 ? 2 : 1)
         const float kk[2] = {ks * scl[c][0], ks * scl[c][1]};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float x = sc[c][0][i] + sc[c][1][i];
-          if (BIAS) {
-            x *= kk[i & 1];
-            if (a.softcap > 0.f) x = kv8_cap(x, a.softcap);
-            x = fmaf(x, kLog2e, lv) -
-                slope[c][i & 1] * static_cast<float>(abs(row[c][i & 1].pos - key0 - kg - 8 * (i >> 1)));
-          } else {
-            x = fmaf(x, kk[i & 1], lv);
+          z[i] = sc[c][0][i] + sc[c][1][i];
+          if (!BIAS) z[i] = fmaf(z[i], kk[i & 1], lv);
+        }
+        if (BIAS) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) z[i] *= kk[i & 1];
+          if (a.softcap > 0.f)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) z[i] = kv8_cap(z[i], a.softcap, two_over_cap);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float gap = static_cast<float>(row[c][e].pos - key0 - kg);
+            z[e] = fmaf(-slope[c][e], fabsf(gap), fmaf(z[e], kLog2e, lv));
+            z[2 + e] = fmaf(-slope[c][e], fabsf(gap - 8.f), fmaf(z[2 + e], kLog2e, lv));
           }
-          z[i] = x;
         }
         if (!whole) {
 #pragma unroll

@@ -138,7 +138,7 @@ struct TileSoftmax {
   int tile;
   Kv8Row row;
   float scl, slope;  // row scale times the softmax scale (natural units); slope in log2 units
-  float m, l;
+  float m, l, two_over_cap;
 
   // The scores of 32 columns (cells 2c, 2c + 1) as z; returns their maximum.
   __device__ __forceinline__ float scores(const TileMeta& M, int c, uint32_t (&r)[32]) {
@@ -152,7 +152,7 @@ struct TileSoftmax {
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         float x = __uint_as_float(r[gq * 16 + i]) * kk;
-        if (BIAS && a.softcap > 0.f) x = kv8_cap(x, a.softcap);
+        if (BIAS && a.softcap > 0.f) x = kv8_cap(x, a.softcap, two_over_cap);
         x = fmaf(x, kLog2e, lv);
         if (BIAS) x -= slope * static_cast<float>(abs(row.pos - key0 - i));
         if (!((bits >> i) & 1u)) x = -INFINITY;
@@ -352,7 +352,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       TileSoftmax<D, BIAS> sm{a, seq, metas, &bars, &abort_flag, (tmem + 128 * tile) | lanes,
                               (tmem + 256 + D * tile) | lanes, tile, kv8_row(a, seq, rr / a.group),
                               qscale[min(r, r1 - 1 - r0)],
-                              a.slopes ? a.slopes[h * a.group + rr % a.group] * kLog2e : 0.f, kNoMax, 0.f};
+                              a.slopes ? a.slopes[h * a.group + rr % a.group] * kLog2e : 0.f, kNoMax, 0.f,
+                              BIAS && a.softcap > 0.f ? 2.0f * kLog2e / a.softcap : 0.f};
       bool ok = sm.run(n);
       if (ok && n > 0) ok = __all_sync(~0u, mbar_wait(smem_u32(&bars.o_full[tile]), 0, &abort_flag));
       tc_fence_after();
@@ -478,7 +479,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     int sent_k = 0, sent_v = 0;
     for (int j = 0; j < n; ++j) {
       // lanes 0-7: the tile's cells
-      const int v = v0 + j * kTileCells + lane;
+      const int v = v0 + (n - 1 - j) * kTileCells + lane;  // from the nearest keys to the farthest
       int key0 = INT_MAX / 2, row = -1;
       float2 sc = make_float2(0.f, 1.f);
       if (lane < kTileCells && v < v1) {
