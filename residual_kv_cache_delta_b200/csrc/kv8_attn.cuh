@@ -23,7 +23,7 @@ static Kv8Plan kv8_plan(const dkv_kv8_shape& sh, int num_seqs, int max_q, int sp
   const int per_sm = sh.dtype == DKV_F32 ? 4 : p.tile == 8 ? 2 : 1;
   const int64_t base = ceil_div64(rows, p.tile) * sh.num_kv_heads * std::max(num_seqs, 1);
   const int64_t cells = ceil_div64(span, kKv8CellKeys);
-  const int64_t sms = num_sms();
+  const int64_t sms = tiles ? num_sms() / 2 : num_sms();  // the tcgen05 kernel's CTAs come in pairs
   const int most = static_cast<int>(std::max<int64_t>(
       1, std::min<int64_t>(kKv8MaxSplits, ceil_div64(cells, kKv8MinSplitCells))));
   // Time in cells of one SM: the fullest SM's share of the cells, a start and an end for each of its rounds of CTAs, and
@@ -75,12 +75,10 @@ template <int D, bool E4M3, bool BIAS>
 static dkv_status attn_tile(const Kv8Attn& p, cudaStream_t st) {
   constexpr auto kKernel = kv8_tile_kernel<D, E4M3, BIAS>;
   if (!ensure_max_dynamic_smem<kKernel>()) return DKV_ERR_CUDA;
-  CUtensorMap map;
-  if (!make_map_codes(&map, p.codes, static_cast<uint64_t>(p.num_blocks) * p.heads * 2 * p.block, D)) return DKV_ERR_CUDA;
   const int row_tiles = static_cast<int>(ceil_div64(static_cast<int64_t>(p.max_q) * p.group, kTileRows));
-  const int64_t ctas = static_cast<int64_t>(p.nsplit) * row_tiles * p.heads * p.num_seqs;
-  if (ctas > INT32_MAX) return DKV_ERR_UNSUPPORTED;
-  kKernel<<<static_cast<unsigned>(ctas), kTileThreads, TileSmem<D>::bytes, st>>>(map, p, row_tiles);
+  const int64_t ctas = static_cast<int64_t>(p.nsplit) * row_tiles * p.heads * p.num_seqs;  // pairs
+  if (ctas > INT32_MAX / 2) return DKV_ERR_UNSUPPORTED;
+  kKernel<<<static_cast<unsigned>(2 * ctas), kTileThreads, TileSmem<D>::bytes, st>>>(p, row_tiles);
   if (cudaGetLastError() != cudaSuccess) return DKV_ERR_CUDA;
   return launch_combine<__nv_bfloat16, D>(p, st);
 }

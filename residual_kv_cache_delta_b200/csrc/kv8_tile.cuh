@@ -1,71 +1,81 @@
 // Attention over the 8-bit cache for many query rows (prefill chunks, packed prompts) on tcgen05.
 //
-// A CTA takes up to 256 rows (a row is a query token and a head of the kv head's group) as two tiles of 128, and a range
-// of keys in tiles of 128 (eight 16-key cells).  Per key tile and row tile
-//   S = Q K^T (M = 128 rows, N = 128 keys, K = d),   P = 2^(z - m),   O += P V (N = d, K = 128 keys),
-// S and O in tensor memory, P written over S as fp16 and read by the second MMA from there.  Roles:
+// A pair of CTAs takes up to 512 rows (a row is a query token and a head of the kv head's group) as two row tiles of 256,
+// 128 of each tile's rows per CTA, and a range of keys in tiles of 128 (eight 16-key cells).  Per key tile and row tile
+//   S = Q K^T (M = 256 rows, N = 128 keys, K = d),   P = 2^(z - m),   O += P V (N = d, K = 128 keys)
+// as pair MMAs (cta_group::2), S and O in tensor memory, P written over S as fp16 and read by the second MMA from
+// there.  Each CTA makes half of the shared operands: 64 keys of K, half of V's dimensions.  With one CTA per tile the
+// shared memory that feeds S (M = N = 128, both operands from there) is the limit: 117 clocks per 128 x 128 x 16 MMA
+// measured against 64 for the pair's 256 x 128 x 16, and every code is converted twice.  Roles in each CTA:
 //   warps 0-3, 4-7  softmax of row tile 0 and 1: a thread owns a row (a tensor-memory lane)
-//   warps 8-11      turn codes into fp16 operands in shared memory; K and V, which lie alike (keys by 64-dimension
-//                   panels of 128 bytes, 128-byte swizzle), are a K-major and an MN-major operand
-//   warp 12         issues the MMAs;  warp 13 loads codes (tensor-map boxes of 16 rows), scales and block ids
-// While one row tile is in its softmax the tensor cores work for the other.
+//   warps 8-11      load codes into registers, a key tile ahead, and turn them into fp16 operands in shared memory; K and V,
+//                   which lie alike (rows of keys), are a K-major and an MN-major operand
+//   warp 12         issues the MMAs (first CTA);  warp 13 looks up block ids and scales, four key tiles at a time
+// The softmax warps take registers from the others (184 against 96 and 48), so that a thread holds its row's 128 scores and
+// tensor memory is read once per key tile.  While one row tile is in its softmax the tensor cores work for the other.
 //
 // Codes are exact in fp16; scales stay out of the operands as in kv8_stream.cuh: the K scale multiplies the fp32 score,
 // the V scale is part of the exponent z = score + log2(v scale), and the sum of weights takes it out again.  The running
-// maximum is raised (and O rescaled in tensor memory) only when a row passes it by more than 2^4.
+// maximum is raised (and O rescaled in tensor memory) only when a row passes it by more than 2^8.
 #pragma once
 
+#include "kv8_append.cuh"
 #include "kv8_stream.cuh"
 
 namespace dkv {
 
-constexpr int kTileThreads = 448, kTileRows = 256, kTileKeys = 128, kTileCells = kTileKeys / kKv8CellKeys;
-constexpr int kMetaSlots = 4;
+constexpr int kTileThreads = 512, kTileRows = 512, kTileKeys = 128, kTileCells = kTileKeys / kKv8CellKeys;
+constexpr int kTileStages = 3;       // of K and of V
+constexpr float kTileSlack = 8.0f;   // log2 of the most a weight may exceed 1 before the maximum is raised (fp16: 2^16)
+// Key tiles looked up at a time (a lane per cell), and how many such batches are kept.
+constexpr int kMetaBatch = 32 / kTileCells, kMetaBatches = 4, kMetaSlots = kMetaBatch * kMetaBatches;
 
-struct TileMeta {  // of one key tile: per cell the first key, K scale, log2 and inverse of the V scale; mapped cells
-  int key0[kTileCells];
-  float ks[kTileCells], lv[kTileCells], iv[kTileCells];
-  int there, pad[3];
+struct TileMeta {  // of one key tile
+  int64_t at[kTileCells];  // byte offset of a cell's K codes
+  int key0[kTileCells];    // its first key
+  float ks[kTileCells], lv[kTileCells], iv[kTileCells];  // K scale, log2 and inverse of the V scale
+  int there, pad[3];       // cells that are mapped
 };
 
-// Bytes of shared memory: Q, two stages of fp16 K and V, one stage of codes.
+// Bytes of a CTA's shared memory: 256 rows of Q, its halves of K and V as fp16.
 template <int D>
 struct TileSmem {
-  static constexpr uint32_t kOperand = kTileKeys * D * 2;  // an fp16 operand of 128 rows
-  static constexpr uint32_t kRaw = kTileKeys * D;          // 128 rows of codes
-  static constexpr uint32_t q = 0, k = q + 2 * kOperand, v = k + 2 * kOperand, rk = v + 2 * kOperand, rv = rk + kRaw;
-  static constexpr uint32_t total = rv + kRaw;
+  static constexpr uint32_t kQ = 128 * D * 2, kHalf = kTileKeys * D;
+  static constexpr uint32_t q = 0, k = q + 2 * kQ, v = k + kTileStages * kHalf, total = v + kTileStages * kHalf;
   static constexpr size_t bytes = 1024 + total;
 };
 
 struct TileBars {
-  uint64_t rk_full, rk_empty, rv_full, rv_empty;
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t s_full[2], p_full[2], o_full[2], drain;
+  uint64_t meta_full[kMetaBatches], meta_empty[kMetaBatches];
+  uint64_t k_full[kTileStages], v_full[kTileStages], p_full[2];    // of the pair, in the first CTA: both CTAs arrive
+  uint64_t k_empty[kTileStages], v_empty[kTileStages], s_full[2], o_full[2], drain;  // in both: the MMAs' commits arrive
 };
+constexpr int kTileBars = sizeof(TileBars) / 8;
 
-// Matrix descriptor of an MN-major operand in 64-element panels of 128-byte rows with the 128-byte swizzle: 8-row groups
-// 1024 bytes apart (stride), panels `panel` bytes apart (leading).
-__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t smem_addr, uint32_t panel) {
+// Matrix descriptor of an MN-major operand of one panel: rows (along K) of 64 elements with the 128-byte swizzle or 32 with
+// the 64-byte one, 8-row groups contiguous (stride).
+template <int ELEMS>
+__device__ __forceinline__ uint64_t mnmajor_desc(uint32_t smem_addr) {
+  static_assert(ELEMS == 64 || ELEMS == 32, "a 128-byte or a 64-byte row");
   uint64_t d = 0;
   d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>(panel >> 4) << 16;
-  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 16;
+  d |= static_cast<uint64_t>((8u * ELEMS * 2u) >> 4) << 32;
   d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(2u) << 61;
+  d |= static_cast<uint64_t>(ELEMS == 64 ? 2u : 4u) << 61;
   return d;
 }
 // kind::f16, D fp32, A and B fp16; b_mn: B is MN-major.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn) {
   return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
-// D[tmem] (+)= A[tmem] * B[smem].
-__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                            uint32_t accumulate) {
+// D[tmem] (+)= A[tmem] * B[smem] of the pair.
+__device__ __forceinline__ void umma_f16_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
+                                                 uint32_t accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
@@ -77,17 +87,18 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
-__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
-}
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// Register shares of the warpgroups; all warps of one execute it together.
+template <int N>
+__device__ __forceinline__ void regs_take() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_give() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 
 // Bits lo .. hi-1 (clamped to 0 .. 32).
 __device__ __forceinline__ uint32_t bit_range(int lo, int hi) {
@@ -101,32 +112,75 @@ __device__ __forceinline__ uint32_t cell_bits(const Kv8Row& r, int prefix, int k
   return b & 0xffffu;
 }
 
-template <int D, bool E4M3>
-__device__ __forceinline__ void convert_tile(const uint8_t* raw, uint8_t* dst, const TileMeta* zero_from, int T) {
-  const int tid = threadIdx.x - 256;  // 128 threads: a thread per row
-  constexpr int kChunks = D / 16;
-  const int r = tid;
-  bool clear = false;
-  if (zero_from) {  // V rows of no key: weight 0 times them must stay 0, and e4m3 bytes may be NaN
-    const int c = r / kKv8CellKeys;
-    clear = !((zero_from->there >> c) & 1) || zero_from->key0[c] + r % kKv8CellKeys >= T;
-  }
+// 16 codes as 32 bytes of fp16, stored as the 16-byte chunks ch and ch + 1 of a row whose chunks are permuted by `swz`;
+// swap: in the other order (so that eight lanes of a store cover all banks).
+template <bool E4M3>
+__device__ __forceinline__ void store_codes(uint8_t* row, int ch, int swz, int swap, const uint4& v) {
+  const uint32_t x[4] = {flip_sign<E4M3>(v.x), flip_sign<E4M3>(v.y), flip_sign<E4M3>(v.z), flip_sign<E4M3>(v.w)};
+  uint32_t y[8];
 #pragma unroll
-  for (int c = 0; c < kChunks; ++c) {
-    uint4 w = *reinterpret_cast<const uint4*>(raw + stream_chunk<D>(r, c));
-    if (clear) w = make_uint4(0u, 0u, 0u, 0u);
-    const uint32_t x[4] = {flip_sign<E4M3>(w.x), flip_sign<E4M3>(w.y), flip_sign<E4M3>(w.z), flip_sign<E4M3>(w.w)};
-    uint32_t y[8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) y[2 * i] = codes_f16<E4M3, false>(x[i]), y[2 * i + 1] = codes_f16<E4M3, true>(x[i]);
-    uint8_t* p = dst + (c / 4) * (kTileKeys * 128) + r * 128;
-    const int ch = (c % 4) * 2;
-    *reinterpret_cast<uint4*>(p + ((ch ^ (r & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-    *reinterpret_cast<uint4*>(p + (((ch + 1) ^ (r & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
-  }
+  for (int k = 0; k < 4; ++k) y[2 * k] = codes_f16<E4M3, false>(x[k]), y[2 * k + 1] = codes_f16<E4M3, true>(x[k]);
+  const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
+  *reinterpret_cast<uint4*>(row + (((ch + swap) ^ swz) << 4)) = swap ? hi : lo;
+  *reinterpret_cast<uint4*>(row + (((ch + 1 - swap) ^ swz) << 4)) = swap ? lo : hi;
+}
+__device__ __forceinline__ uint4 load_codes16(const uint8_t* p) {
+  uint4 w;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
+               : "l"(p));
+  return w;
 }
 
-// Softmax of one row tile by its four warps.  BIAS: scores may be capped or biased.
+// A converter warp's share of a CTA's half of a key tile, in registers: K rows 64 rank + 16 warp .. + 15, all dimensions; V
+// rows 32 warp .. + 31, dimensions (d / 2) rank .. + d / 2.
+template <int D>
+struct TileCodes {
+  static constexpr int kKLanes = D / 16, kKRows = 32 / kKLanes, kVLanes = D / 32, kVRows = 32 / kVLanes;
+  uint4 k[16 / kKRows], v[32 / kVRows];
+
+  __device__ __forceinline__ void load_k(const uint8_t* codes, const TileMeta& M, int rank, int warp, int lane) {
+    const int cell = 4 * rank + warp;  // 16 rows of one cell
+#pragma unroll
+    for (int i = 0; i < 16 / kKRows; ++i) {
+      k[i] = make_uint4(0u, 0u, 0u, 0u);
+      if ((M.there >> cell) & 1)
+        k[i] = load_codes16(codes + M.at[cell] + (i * kKRows + lane / kKLanes) * D + (lane % kKLanes) * 16);
+    }
+  }
+  __device__ __forceinline__ void load_v(const uint8_t* codes, const TileMeta& M, int rank, int warp, int lane) {
+#pragma unroll
+    for (int i = 0; i < 32 / kVRows; ++i) {
+      const int r = 32 * warp + i * kVRows + lane / kVLanes, cell = r / kKv8CellKeys;
+      v[i] = make_uint4(0u, 0u, 0u, 0u);
+      if ((M.there >> cell) & 1)
+        v[i] = load_codes16(codes + M.at[cell] + (r % kKv8CellKeys) * D + rank * (D / 2) + (lane % kVLanes) * 16);
+    }
+  }
+  template <bool E4M3>
+  __device__ __forceinline__ void store_k(uint8_t* dst, int warp, int lane) const {  // panels of 64 rows of 128 bytes
+    const int c = lane % kKLanes;
+#pragma unroll
+    for (int i = 0; i < 16 / kKRows; ++i) {
+      const int r = 16 * warp + i * kKRows + lane / kKLanes;
+      store_codes<E4M3>(dst + (c / 4) * (64 * 128) + r * 128, (c % 4) * 2, r & 7, c / 4, k[i]);
+    }
+  }
+  // Rows of no key, from T on, are stored as 0: weight 0 times them must stay 0, and e4m3 bytes may be NaN.
+  template <bool E4M3>
+  __device__ __forceinline__ void store_v(uint8_t* dst, const TileMeta& M, int T, int warp, int lane) const {
+    const int c = lane % kVLanes;  // rows of d / 2 fp16: 128 or 64 bytes
+#pragma unroll
+    for (int i = 0; i < 32 / kVRows; ++i) {
+      const int r = 32 * warp + i * kVRows + lane / kVLanes;
+      uint4 x = v[i];
+      if (M.key0[r / kKv8CellKeys] + r % kKv8CellKeys >= T) x = make_uint4(0u, 0u, 0u, 0u);
+      store_codes<E4M3>(dst + r * D, 2 * c, D == 128 ? r & 7 : (r >> 1) & 3, 0, x);
+    }
+  }
+};
+
+// Softmax of a CTA's 128 rows of one row tile by four warps.  BIAS: scores may be capped or biased.
 template <int D, bool BIAS>
 struct TileSoftmax {
   const Kv8Attn& a;
@@ -135,133 +189,179 @@ struct TileSoftmax {
   TileBars* bars;
   volatile int* abort_flag;
   uint32_t s_tmem, o_tmem;  // of this warp's lanes
+  uint32_t p_full;          // cluster address of the pair's barrier
   int tile;
   Kv8Row row;
   float scl, slope;  // row scale times the softmax scale (natural units); slope in log2 units
-  float m, l, two_over_cap;
+  float m, l;
 
-  // The scores of 32 columns (cells 2c, 2c + 1) as z; returns their maximum.
-  __device__ __forceinline__ float scores(const TileMeta& M, int c, uint32_t (&r)[32]) {
+  // The scores of cell `cell` (16 columns) as z, in place; returns their maximum.
+  __device__ __forceinline__ float scores(const TileMeta& M, int cell, uint32_t* r, float two_over_cap) {
+    float top = -INFINITY;
+    const int key0 = M.key0[cell];
+    const float kk = M.ks[cell] * scl, lv = M.lv[cell];
+    uint32_t bits = cell_bits(row, seq.prefix, key0);
+    if (!((M.there >> cell) & 1)) bits = 0;
+    const float gap = static_cast<float>(row.pos - key0);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float x = __uint_as_float(r[i]) * kk;
+      if (BIAS && a.softcap > 0.f) x = kv8_cap(x, a.softcap, two_over_cap);
+      x = fmaf(x, kLog2e, lv);
+      if (BIAS) x = fmaf(-slope, fabsf(gap - static_cast<float>(i)), x);
+      if (!((bits >> i) & 1u)) x = -INFINITY;
+      r[i] = __float_as_uint(x);
+      top = fmaxf(top, x);
+    }
+    return top;
+  }
+
+  // The same where every key is seen and stands at or before the row's position, two columns to an instruction.  Capped
+  // scores: tanh(y) = y P(y^2) with a polynomial (Chebyshev interpolation of degree 4 in y^2 on [0, 0.36], relative error
+  // 7.2e-8), where exp2 and a reciprocal would keep the special-function unit for three times as long as the softmax's own
+  // exp2 does; `most` is raised to the largest y^2, which must stay within 0.36.
+  __device__ __forceinline__ float scores_quick(const TileMeta& M, int cell, uint32_t* r, float& most) {
+    const float lv = fmaf(-slope, static_cast<float>(row.pos - M.key0[cell]), M.lv[cell]);
+    const bool cap = a.softcap > 0.f;
+    const float kk = cap ? M.ks[cell] * scl / a.softcap : M.ks[cell] * scl * kLog2e, out = a.softcap * kLog2e;
+    const uint64_t kk2 = pack2(kk, kk), out2 = pack2(out, out), lv2 = pack2(lv, lv), sl2 = pack2(slope, slope);
     float top = -INFINITY;
 #pragma unroll
-    for (int gq = 0; gq < 2; ++gq) {
-      const int cell = 2 * c + gq, key0 = M.key0[cell];
-      const float kk = M.ks[cell] * scl, lv = M.lv[cell];
-      uint32_t bits = cell_bits(row, seq.prefix, key0);
-      if (!((M.there >> cell) & 1)) bits = 0;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        float x = __uint_as_float(r[gq * 16 + i]) * kk;
-        if (BIAS && a.softcap > 0.f) x = kv8_cap(x, a.softcap, two_over_cap);
-        x = fmaf(x, kLog2e, lv);
-        if (BIAS) x -= slope * static_cast<float>(abs(row.pos - key0 - i));
-        if (!((bits >> i) & 1u)) x = -INFINITY;
-        r[gq * 16 + i] = __float_as_uint(x);
-        top = fmaxf(top, x);
+    for (int i = 0; i < 16; i += 2) {
+      uint64_t y = mul2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), kk2);
+      float x0, x1;
+      if (cap) {
+        const uint64_t u = mul2(y, y);
+        unpack2(u, x0, x1);
+        most = fmaxf(fmaxf(most, x0), x1);
+        uint64_t p = fma2(u, pack2(0.01548669021576643f, 0.01548669021576643f), pack2(-0.052109625190496445f, -0.052109625190496445f));
+        p = fma2(u, p, pack2(0.13310357928276062f, 0.13310357928276062f));
+        p = fma2(u, p, pack2(-0.33332324028015137f, -0.33332324028015137f));
+        p = fma2(u, p, pack2(0.9999999403953552f, 0.9999999403953552f));
+        y = mul2(mul2(y, p), out2);
       }
+      y = add2(y, fma2(sl2, pack2(static_cast<float>(i), static_cast<float>(i + 1)), lv2));
+      unpack2(y, x0, x1);
+      r[i] = __float_as_uint(x0), r[i + 1] = __float_as_uint(x1);
+      top = fmaxf(fmaxf(top, x0), x1);
     }
     return top;
   }
 
   __device__ __forceinline__ bool run(int n) {
+    const float two_over_cap = BIAS && a.softcap > 0.f ? 2.0f * kLog2e / a.softcap : 0.f;
     for (int j = 0; j < n; ++j) {
-      if (!__all_sync(~0u, mbar_wait(smem_u32(&bars->s_full[tile]), j & 1, abort_flag))) return false;
+      bool ok = true;
+      if (j % kMetaBatch == 0)
+        ok = mbar_wait(smem_u32(&bars->meta_full[j / kMetaBatch % kMetaBatches]), (j / kMetaSlots) & 1, abort_flag);
+      if (!__all_sync(~0u, ok && mbar_wait(smem_u32(&bars->s_full[tile]), j & 1, abort_flag))) return false;
       tc_fence_after();
       const TileMeta& M = metas[j % kMetaSlots];
+      uint32_t r[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(s_tmem + 32 * c, r[c]);
       const int k0 = M.key0[0], k1 = M.key0[kTileCells - 1] + kKv8CellKeys - 1;
-      // quick: every key of the tile is seen by all of the warp's rows and z is one fused multiply-add of the raw score,
-      // done again in the second pass.  m then is not the exact maximum of those sums, but within a rounding of
-      // it, so scores whose rounding is not small against 1 take the other path.
-      bool quick = !BIAS && __all_sync(~0u, M.there == (1 << kTileCells) - 1 && k1 - k0 == kTileKeys - 1 &&
-                                                      row.lo <= k0 && k1 <= row.hi);
+      // quick: every key of the tile is seen by all of the warp's rows and, without a bias, z is one fused multiply-add of
+      // the raw score, done again in the second pass.  m then is not the exact maximum of those sums, but
+      // within a rounding of it, so scores whose rounding is not small against 1 take the other path.
+      bool quick = __all_sync(~0u, M.there == (1 << kTileCells) - 1 && k1 - k0 == kTileKeys - 1 && row.lo <= k0 &&
+                                       k1 <= row.hi);
       float top = -INFINITY;
-      uint32_t r[32];
-      if (quick) {
+      tmem_ld_wait();
+      if (quick && BIAS) {
+        float most = 0.f;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_ld_32x32b_x32(s_tmem + 32 * c, r);
+        for (int cell = 0; cell < kTileCells; ++cell)
+          top = fmaxf(top, scores_quick(M, cell, &r[cell / 2][16 * (cell % 2)], most));
+        quick = __all_sync(~0u, most <= 0.36f);
+        if (!quick) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(s_tmem + 32 * c, r[c]);
           tmem_ld_wait();
+        }
+      } else if (quick) {
 #pragma unroll
-          for (int gq = 0; gq < 2; ++gq) {
-            float x = __uint_as_float(r[16 * gq]);
+        for (int cell = 0; cell < kTileCells; ++cell) {
+          const uint32_t* x = &r[cell / 2][16 * (cell % 2)];
+          float y = __uint_as_float(x[0]);
 #pragma unroll
-            for (int i = 1; i < 16; ++i) x = fmaxf(x, __uint_as_float(r[16 * gq + i]));
-            top = fmaxf(top, fmaf(x, M.ks[2 * c + gq] * scl * kLog2e, M.lv[2 * c + gq]));
-          }
+          for (int i = 1; i < 15; i += 2) y = fmaxf(fmaxf(y, __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
+          y = fmaxf(y, __uint_as_float(x[15]));
+          top = fmaxf(top, fmaf(y, M.ks[cell] * scl * kLog2e, M.lv[cell]));
         }
         quick = __all_sync(~0u, fabsf(top) < 65536.0f);
       }
       if (!quick) {
         top = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          tmem_ld_32x32b_x32(s_tmem + 32 * c, r);
-          tmem_ld_wait();
-          top = fmaxf(top, scores(M, c, r));
-          tmem_st_32x32b_x32(s_tmem + 32 * c, r);  // z in place of the raw score
-        }
-        tmem_st_wait();
+        for (int cell = 0; cell < kTileCells; ++cell)
+          top = fmaxf(top, scores(M, cell, &r[cell / 2][16 * (cell % 2)], two_over_cap));
       }
-      const bool rise = top > m + kMaxSlack;
+      const bool rise = top > m + kTileSlack;
       if (__any_sync(~0u, rise)) {
         const float now = rise ? top : m, fix = fast_exp2(m - now);
         m = now;
         l *= fix;
         if (j > 0) {
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            tmem_ld_32x32b_x32(o_tmem + 32 * c, r);
+#pragma unroll 1
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t x[16];
+            tmem_ld_32x32b_x16(o_tmem + 16 * c, x);
             tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * fix);
-            tmem_st_32x32b_x32(o_tmem + 32 * c, r);
+            for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * fix);
+            tmem_st_32x32b_x16(o_tmem + 16 * c, x);
           }
         }
       }
+      const bool raw = quick && !BIAS;  // r still holds the raw scores
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         uint32_t p[16];
-        tmem_ld_32x32b_x32(s_tmem + 32 * c, r);
-        tmem_ld_wait();
 #pragma unroll
         for (int gq = 0; gq < 2; ++gq) {
           const int cell = 2 * c + gq;
-          const float kk = quick ? M.ks[cell] * scl * kLog2e : 1.0f, add = quick ? M.lv[cell] - m : -m;
-          const float iv = M.iv[cell];
-          float sum = 0.f;
+          const float kk = raw ? M.ks[cell] * scl * kLog2e : 1.0f, add = raw ? M.lv[cell] - m : -m;
+          const uint64_t kk2 = pack2(kk, kk), add_2 = pack2(add, add);
+          uint64_t sum2 = 0;
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
-            const float x = fast_exp2(fmaf(__uint_as_float(r[gq * 16 + i]), kk, add));
-            const float y = fast_exp2(fmaf(__uint_as_float(r[gq * 16 + i + 1]), kk, add));
-            sum += x + y;
+            float x, y;
+            unpack2(fma2(pack2(__uint_as_float(r[c][gq * 16 + i]), __uint_as_float(r[c][gq * 16 + i + 1])), kk2, add_2), x, y);
+            x = fast_exp2(x), y = fast_exp2(y);
+            sum2 = add2(sum2, pack2(x, y));
             p[gq * 8 + i / 2] = pack_f16(x, y);
           }
-          if (sum != 0.f) l = fmaf(sum, iv, l);  // a cell out of sight adds nothing, even where its scale is NaN
+          float x, y;
+          unpack2(sum2, x, y);
+          x += y;
+          if (x != 0.f) l = fmaf(x, M.iv[cell], l);  // a cell out of sight adds nothing, even where its scale is NaN
         }
         tmem_st_32x32b_x16(s_tmem + 16 * c, p);
       }
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane_id() == 0) mbar_arrive(smem_u32(&bars->p_full[tile]));
+      if (lane_id() == 0) mbar_arrive_cluster(p_full);
     }
     return true;
   }
 };
 
 template <int D, bool E4M3, bool BIAS>
-__global__ void __launch_bounds__(kTileThreads, 1)
-    kv8_tile_kernel(const __grid_constant__ CUtensorMap map, const Kv8Attn a, int row_tiles) {
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
+    kv8_tile_kernel(const __grid_constant__ Kv8Attn a, int row_tiles) {
   using L = TileSmem<D>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) TileBars bars;
   __shared__ TileMeta metas[kMetaSlots];
-  __shared__ float qscale[kTileRows];
+  __shared__ float qscale[256];
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
   uint8_t* smem = align_shared<1024>(smem_raw);
 
-  int64_t id = blockIdx.x;
+  int64_t id = blockIdx.x / 2;
+  const int rank = static_cast<int>(cluster_ctarank());
   const int split = static_cast<int>(id % a.nsplit);
   id /= a.nsplit;
   const int s = static_cast<int>(id % a.num_seqs);
@@ -271,25 +371,24 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   griddep_launch_dependents();
   const Kv8Seq seq = kv8_seq(a, s);
   const int nrows = seq.nq * a.group, r0 = rt * kTileRows;
-  if (!seq.ok || r0 >= nrows) return;
+  if (!seq.ok || r0 >= nrows) return;  // the same for both CTAs
   const int r1 = min(r0 + kTileRows, nrows), hq = a.heads * a.group;
-  const int tiles = r1 - r0 > 128 ? 2 : 1;
+  const int tiles = r1 - r0 > 256 ? 2 : 1;
   const int i0 = r0 / a.group, i1 = (r1 - 1) / a.group;
   const int warp = warp_id(), lane = lane_id();
+  // global row of this CTA's row r (0 .. 255): row tile r / 128, this CTA's half of it
+  auto global_row = [&](int r) { return r0 + (r / 128) * 256 + rank * 128 + r % 128; };
 
   if (threadIdx.x == 0) {
     abort_flag = 0;
     const uint32_t b = smem_u32(&bars);
-    constexpr int kCounts[] = {1, 4, 1, 4, 4, 4, 1, 1, 4, 4, 1, 1, 1, 1, 4, 4, 1, 1, 1};
-    static_assert(sizeof(TileBars) == sizeof(kCounts) / 4 * 8, "one count per barrier");
-#pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(TileBars) / 8); ++i) mbar_init(b + 8 * i, kCounts[i]);
+    constexpr int kPair = 2 * kMetaBatches, kLocal = kPair + 2 * kTileStages + 2;  // barriers that 8 warps of the pair arrive on
+    for (int i = 0; i < kTileBars; ++i) mbar_init(b + 8 * i, i >= kPair && i < kLocal ? 8 : 1);
     fence_barrier_init();
-    prefetch_tensormap(&map);
   }
   if (warp == 12) {
-    tmem_alloc(smem_u32(&tmem_base), 512);
-    tmem_relinquish();
+    tmem_alloc_pair(smem_u32(&tmem_base), 512);
+    tmem_relinquish_pair();
   }
   int first = 0;
   if (a.first_key) {
@@ -303,12 +402,14 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   const int n = (v1 - v0 + kTileCells - 1) / kTileCells;  // key tiles
 
   // Q as fp16, rows scaled by powers of two; four threads a row
+#pragma unroll 2
   for (int r = threadIdx.x / 4; r < tiles * 128; r += kTileThreads / 4) {
-    const int part = threadIdx.x % 4;
+    const int part = threadIdx.x % 4, rr = global_row(r);
     constexpr int kVecs = D / 32;  // 16-byte vectors of a thread
-    uint4 w[kVecs] = {};
-    if (r0 + r < r1) {
-      const int rr = r0 + r;
+    uint4 w[kVecs];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) w[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (rr < r1) {
       const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(a.q) + (seq.q0 + rr / a.group) * a.q_stride +
                                  (h * a.group + rr % a.group) * D + part * (D / 4);
 #pragma unroll
@@ -328,7 +429,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const float down = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);
     if (part == 0)
       qscale[r] = top >= 0x7f800000u ? NAN : __uint_as_float(static_cast<uint32_t>(ex) << 23) * a.scale;
-    uint8_t* dst = smem + L::q + (r / 128) * L::kOperand + (r % 128) * 128;
+    uint8_t* dst = smem + L::q + (r / 128) * L::kQ + (r % 128) * 128;
 #pragma unroll
     for (int i = 0; i < kVecs; ++i) {
       uint32_t y[4];
@@ -341,19 +442,133 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   fence_proxy_async_shared();
   tc_fence_before();
   __syncthreads();
+  cluster_sync_all();  // barriers of both CTAs initialised, both halves of Q in place, tensor memory allocated
   tc_fence_after();
   const uint32_t tmem = tmem_base;
 
+  auto issue_mmas = [&]() {  // one thread of the first CTA
+    constexpr uint32_t kIdS = idesc_f16_f32(256, kTileKeys, false), kIdO = idesc_f16_f32(256, D, true);
+    const uint32_t sb = smem_u32(smem);
+    auto scores = [&](int t, int j) {
+      const uint32_t qa = sb + L::q + t * L::kQ, ka = sb + L::k + (j % kTileStages) * L::kHalf;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+        umma_bf16_pair(tmem + 128 * t, sw128_kmajor_desc(qa + (i / 4) * (128 * 128) + (i % 4) * 32),
+                       sw128_kmajor_desc(ka + (i / 4) * (64 * 128) + (i % 4) * 32), kIdS, i > 0);
+      umma_commit_pair(smem_u32(&bars.s_full[t]), 3);
+    };
+    bool ok = mbar_wait_cluster(smem_u32(&bars.k_full[0]), 0, &abort_flag);
+    if (ok) {
+      tc_fence_after();
+      for (int t = 0; t < tiles; ++t) scores(t, 0);
+      umma_commit_pair(smem_u32(&bars.k_empty[0]), 3);
+    }
+    for (int j = 0; ok && j < n; ++j) {
+      const int st = j % kTileStages, nx = (j + 1) % kTileStages;
+      for (int t = 0; ok && t < tiles; ++t) {
+        ok = mbar_wait_cluster(smem_u32(&bars.v_full[st]), (j / kTileStages) & 1, &abort_flag) &&
+             mbar_wait_cluster(smem_u32(&bars.p_full[t]), j & 1, &abort_flag);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t va = sb + L::v + st * L::kHalf;
+#pragma unroll
+        for (int i = 0; i < kTileKeys / 16; ++i)
+          umma_f16_ts_pair(tmem + 256 + D * t, tmem + 128 * t + 8 * i, mnmajor_desc<D / 2>(va + i * (16 * D)), kIdO,
+                           j > 0 || i > 0);
+        if (j + 1 < n) {
+          ok = mbar_wait_cluster(smem_u32(&bars.k_full[nx]), ((j + 1) / kTileStages) & 1, &abort_flag);
+          if (!ok) break;
+          tc_fence_after();
+          scores(t, j + 1);
+        } else {
+          umma_commit_pair(smem_u32(&bars.o_full[t]), 3);
+        }
+      }
+      if (ok) {
+        umma_commit_pair(smem_u32(&bars.v_empty[st]), 3);
+        if (j + 1 < n) umma_commit_pair(smem_u32(&bars.k_empty[nx]), 3);
+        // p_full of both row tiles and CTAs: nobody reads this key tile's scales any more
+        if (j % kMetaBatch == kMetaBatch - 1)
+          for (int c = 0; c < 2; ++c)
+            mbar_arrive_cluster(mapa_shared(smem_u32(&bars.meta_empty[j / kMetaBatch % kMetaBatches]), c));
+      }
+    }
+    // whatever was issued has finished before shared and tensor memory are given up
+    umma_commit_pair(smem_u32(&bars.drain), 3);
+    mbar_drain(smem_u32(&bars.drain), 0);
+  };
+  auto look_up = [&]() {
+    for (int b = 0; b * kMetaBatch < n; ++b) {
+      // lane: cell lane % 8 of key tile 4 b + lane / 8; tiles go from the nearest keys to the farthest
+      const int j = b * kMetaBatch + lane / kTileCells, v = v0 + (n - 1 - j) * kTileCells + lane % kTileCells;
+      int key0 = INT_MAX / 2;
+      int64_t at = -1;
+      float2 sc = make_float2(0.f, 1.f);
+      if (j < n && v < v1) {
+        key0 = span.cell(v) * kKv8CellKeys;
+        const int blk = kv8_block(a.block_tables, a.max_blocks, a.num_blocks, s, key0 / a.block);
+        if (blk >= 0) {
+          const int64_t cell = (static_cast<int64_t>(blk) * a.heads + h) * 2;
+          sc = *reinterpret_cast<const float2*>(a.scales + cell);
+          at = (cell * a.block + key0 % a.block) * D;
+        }
+      }
+      const uint32_t there = __ballot_sync(~0u, at >= 0);
+      if (!__all_sync(~0u, mbar_wait_cluster(smem_u32(&bars.meta_empty[b % kMetaBatches]), ((b / kMetaBatches) & 1) ^ 1,
+                                             &abort_flag)))
+        break;
+      TileMeta& M = metas[j % kMetaSlots];
+      const int c = lane % kTileCells;
+      const float vs = sc.y < kLeastScale ? kLeastScale : sc.y;  // NaN stays
+      M.at[c] = at, M.key0[c] = key0, M.ks[c] = sc.x, M.lv[c] = __log2f(vs), M.iv[c] = __frcp_rn(vs);
+      if (c == 0) M.there = (there >> (lane & ~(kTileCells - 1))) & ((1 << kTileCells) - 1);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&bars.meta_full[b % kMetaBatches]));
+    }
+  };
+  auto convert = [&]() {
+    TileCodes<D> x;
+    const int w = warp - 8;
+    const uint8_t* vcodes = a.codes + static_cast<int64_t>(a.block) * D;
+    for (int j = 0; j <= n; ++j) {  // stores key tile j - 1, loads j
+      if (j < n && j % kMetaBatch == 0 &&
+          !__all_sync(~0u, mbar_wait(smem_u32(&bars.meta_full[j / kMetaBatch % kMetaBatches]),
+                                     (j / kMetaSlots) & 1, &abort_flag)))
+        break;
+      const TileMeta &last = metas[(j + kMetaSlots - 1) % kMetaSlots], &next = metas[j % kMetaSlots];
+      const int st = (j + kTileStages - 1) % kTileStages;
+      const uint32_t free_par = (((j - 1) / kTileStages) & 1) ^ 1;
+      if (j > 0) {
+        if (!__all_sync(~0u, mbar_wait(smem_u32(&bars.k_empty[st]), free_par, &abort_flag))) break;
+        x.template store_k<E4M3>(smem + L::k + st * L::kHalf, w, lane);
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&bars.k_full[st]), 0));
+      }
+      if (j < n) x.load_k(a.codes, next, rank, w, lane);
+      if (j > 0) {
+        if (!__all_sync(~0u, mbar_wait(smem_u32(&bars.v_empty[st]), free_par, &abort_flag))) break;
+        x.template store_v<E4M3>(smem + L::v + st * L::kHalf, last, seq.T, w, lane);
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&bars.v_full[st]), 0));
+      }
+      if (j < n) x.load_v(vcodes, next, rank, w, lane);
+    }
+  };
+
+  // per sub-partition: 2 x 184 + 96 + 48 = 4 x 128 registers a thread, what the CTA was launched with
   if (warp < 8) {
+    regs_take<184>();
     const int tile = warp / 4;
     if (tile < tiles) {
       const uint32_t lanes = static_cast<uint32_t>(warp % 4) << 21;  // (32 * quarter) << 16
-      const int r = tile * 128 + (warp % 4) * 32 + lane, rr = min(r0 + r, r1 - 1);
+      const int r = tile * 128 + (warp % 4) * 32 + lane, rr = min(global_row(r), r1 - 1);
+      const bool mine = global_row(r) < r1;
       TileSoftmax<D, BIAS> sm{a, seq, metas, &bars, &abort_flag, (tmem + 128 * tile) | lanes,
-                              (tmem + 256 + D * tile) | lanes, tile, kv8_row(a, seq, rr / a.group),
-                              qscale[min(r, r1 - 1 - r0)],
-                              a.slopes ? a.slopes[h * a.group + rr % a.group] * kLog2e : 0.f, kNoMax, 0.f,
-                              BIAS && a.softcap > 0.f ? 2.0f * kLog2e / a.softcap : 0.f};
+                              (tmem + 256 + D * tile) | lanes, mapa_shared(smem_u32(&bars.p_full[tile]), 0), tile,
+                              kv8_row(a, seq, rr / a.group), mine ? qscale[r] : 0.f,
+                              a.slopes ? a.slopes[h * a.group + rr % a.group] * kLog2e : 0.f, kNoMax, 0.f};
       bool ok = sm.run(n);
       if (ok && n > 0) ok = __all_sync(~0u, mbar_wait(smem_u32(&bars.o_full[tile]), 0, &abort_flag));
       tc_fence_after();
@@ -371,7 +586,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         if (n == 0 || sum == 0.f)
 #pragma unroll
           for (int i = 0; i < 32; ++i) x[i] = 0u;
-        if (r0 + r < r1) {
+        if (mine) {
           if (a.nsplit > 1) {
             float4* dst = reinterpret_cast<float4*>(a.o + prow * D + 32 * c);
 #pragma unroll
@@ -394,135 +609,26 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           }
         }
       }
-      if (r0 + r < r1) {
+      if (mine) {
         if (a.nsplit > 1) a.ml[prow] = make_float2(sm.m, sum);
         else if (a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (sm.m + log2f(sum)) * kLn2;
       }
       tc_fence_before();
     }
   } else if (warp < 12) {
-    for (int j = 0; j < n; ++j) {
-      const int st = j & 1;
-      const uint32_t free_par = ((j >> 1) & 1) ^ 1;
-      bool ok = mbar_wait(smem_u32(&bars.rk_full), j & 1, &abort_flag) &&
-                mbar_wait(smem_u32(&bars.k_empty[st]), free_par, &abort_flag);
-      if (!__all_sync(~0u, ok)) break;
-      convert_tile<D, E4M3>(smem + L::rk, smem + L::k + st * L::kOperand, nullptr, 0);
-      fence_proxy_async_shared();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(smem_u32(&bars.rk_empty));
-        mbar_arrive(smem_u32(&bars.k_full[st]));
-      }
-      ok = mbar_wait(smem_u32(&bars.rv_full), j & 1, &abort_flag) &&
-           mbar_wait(smem_u32(&bars.v_empty[st]), free_par, &abort_flag);
-      if (!__all_sync(~0u, ok)) break;
-      convert_tile<D, E4M3>(smem + L::rv, smem + L::v + st * L::kOperand, &metas[j % kMetaSlots], seq.T);
-      fence_proxy_async_shared();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(smem_u32(&bars.rv_empty));
-        mbar_arrive(smem_u32(&bars.v_full[st]));
-      }
-    }
-  } else if (warp == 12) {
-    if (lane == 0 && n > 0) {
-      constexpr uint32_t kIdS = idesc_f16_f32(128, kTileKeys, false), kIdO = idesc_f16_f32(128, D, true);
-      const uint32_t sb = smem_u32(smem);
-      auto scores = [&](int tile, int j) {
-        const uint32_t qa = sb + L::q + tile * L::kOperand, ka = sb + L::k + (j & 1) * L::kOperand;
-#pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const uint32_t off = (i / 4) * (128 * 128) + (i % 4) * 32;
-          umma_bf16(tmem + 128 * tile, sw128_kmajor_desc(qa + off), sw128_kmajor_desc(ka + off), kIdS, i > 0);
-        }
-        umma_commit(smem_u32(&bars.s_full[tile]));
-      };
-      bool ok = mbar_wait(smem_u32(&bars.k_full[0]), 0, &abort_flag);
-      if (ok) {
-        tc_fence_after();
-        for (int t = 0; t < tiles; ++t) scores(t, 0);
-        umma_commit(smem_u32(&bars.k_empty[0]));
-      }
-      for (int j = 0; ok && j < n; ++j) {
-        const int st = j & 1;
-        for (int t = 0; ok && t < tiles; ++t) {
-          ok = mbar_wait(smem_u32(&bars.p_full[t]), j & 1, &abort_flag) &&
-               mbar_wait(smem_u32(&bars.v_full[st]), (j >> 1) & 1, &abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t va = sb + L::v + st * L::kOperand;
-#pragma unroll
-          for (int i = 0; i < kTileKeys / 16; ++i)
-            umma_f16_ts(tmem + 256 + D * t, tmem + 128 * t + 8 * i, sw128_mnmajor_desc(va + i * 2048, 128 * 128), kIdO,
-                        j > 0 || i > 0);
-          if (j + 1 < n) {
-            ok = mbar_wait(smem_u32(&bars.k_full[st ^ 1]), ((j + 1) >> 1) & 1, &abort_flag);
-            if (!ok) break;
-            tc_fence_after();
-            scores(t, j + 1);
-          } else {
-            umma_commit(smem_u32(&bars.o_full[t]));
-          }
-        }
-        if (ok) {
-          umma_commit(smem_u32(&bars.v_empty[st]));
-          if (j + 1 < n) umma_commit(smem_u32(&bars.k_empty[st ^ 1]));
-        }
-      }
-      // whatever was issued has finished before shared and tensor memory are given up
-      umma_commit(smem_u32(&bars.drain));
-      mbar_drain(smem_u32(&bars.drain), 0);
-    }
-    __syncwarp();
+    regs_give<96>();
+    convert();
   } else {
-    int sent_k = 0, sent_v = 0;
-    for (int j = 0; j < n; ++j) {
-      // lanes 0-7: the tile's cells
-      const int v = v0 + (n - 1 - j) * kTileCells + lane;  // from the nearest keys to the farthest
-      int key0 = INT_MAX / 2, row = -1;
-      float2 sc = make_float2(0.f, 1.f);
-      if (lane < kTileCells && v < v1) {
-        key0 = span.cell(v) * kKv8CellKeys;
-        const int blk = kv8_block(a.block_tables, a.max_blocks, a.num_blocks, s, key0 / a.block);
-        if (blk >= 0) {
-          const int cell = (blk * a.heads + h) * 2;
-          sc = *reinterpret_cast<const float2*>(a.scales + cell);
-          row = cell * a.block + key0 % a.block;
-        }
-      }
-      const uint32_t there = __ballot_sync(~0u, row >= 0);
-      if (!__all_sync(~0u, mbar_wait(smem_u32(&bars.rk_empty), (j & 1) ^ 1, &abort_flag))) break;
-      TileMeta& M = metas[j % kMetaSlots];
-      if (lane < kTileCells) {
-        const float vs = sc.y < kLeastScale ? kLeastScale : sc.y;  // NaN stays
-        M.key0[lane] = key0, M.ks[lane] = sc.x, M.lv[lane] = __log2f(vs), M.iv[lane] = __frcp_rn(vs);
-        if (lane == 0) M.there = static_cast<int>(there);
-      }
-      __syncwarp();
-      const uint32_t bytes = __popc(there) * kKv8CellKeys * D;
-      if (lane == 0) mbar_arrive_expect_tx(smem_u32(&bars.rk_full), bytes);
-      __syncwarp();
-      if (row >= 0)
-        tma_load_2d(smem_u32(smem) + L::rk + lane * (kKv8CellKeys * D), &map, 0, row, smem_u32(&bars.rk_full));
-      ++sent_k;
-      if (!__all_sync(~0u, mbar_wait(smem_u32(&bars.rv_empty), (j & 1) ^ 1, &abort_flag))) break;
-      if (lane == 0) mbar_arrive_expect_tx(smem_u32(&bars.rv_full), bytes);
-      __syncwarp();
-      if (row >= 0)
-        tma_load_2d(smem_u32(smem) + L::rv + lane * (kKv8CellKeys * D), &map, 0, row + a.block, smem_u32(&bars.rv_full));
-      ++sent_v;
-    }
-    // every copy has landed before the CTA leaves (at once, unless another role gave up)
-    if (lane == 0) {
-      if (sent_k) mbar_drain(smem_u32(&bars.rk_full), (sent_k - 1) & 1);
-      if (sent_v) mbar_drain(smem_u32(&bars.rv_full), (sent_v - 1) & 1);
-    }
+    regs_give<48>();
+    if (warp == 12 && lane == 0 && rank == 0 && n > 0) issue_mmas();
+    __syncwarp();
+    if (warp == 13) look_up();
   }
   __syncthreads();
+  cluster_sync_all();  // neither CTA leaves while the other's MMAs, commits or arrivals may reach it
   if (warp == 12) {
     tc_fence_after();
-    tmem_dealloc(tmem, 512);
+    tmem_dealloc_pair(tmem, 512);
   }
 }
 
