@@ -52,31 +52,35 @@ struct TileBars {
 };
 constexpr int kTileBars = sizeof(TileBars) / 8;
 
-// Matrix descriptor of an MN-major operand of one panel: rows (along K) of 64 elements with the 128-byte swizzle or 32 with
-// the 64-byte one, 8-row groups contiguous (stride).
-template <int ELEMS>
-__device__ __forceinline__ uint64_t mnmajor_desc(uint32_t smem_addr) {
-  static_assert(ELEMS == 64 || ELEMS == 32, "a 128-byte or a 64-byte row");
-  uint64_t d = 0;
-  d |= static_cast<uint64_t>((smem_addr >> 4) & 0x3FFFu);
-  d |= static_cast<uint64_t>(1u) << 16;
-  d |= static_cast<uint64_t>((8u * ELEMS * 2u) >> 4) << 32;
-  d |= static_cast<uint64_t>(1u) << 46;
-  d |= static_cast<uint64_t>(ELEMS == 64 ? 2u : 4u) << 61;
-  return d;
+// Matrix descriptors as two words, so that stepping through an operand is one addition to the low word (address / 16; the
+// leading byte offset, unused by these layouts, is 1): 8-row groups `stride` bytes apart; swizzle 2 = 128 bytes, 4 = 64.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t smem_addr) { return ((smem_addr >> 4) & 0x3FFFu) | 1u << 16; }
+__host__ __device__ constexpr uint32_t desc_hi(uint32_t stride, uint32_t swizzle) {
+  return stride >> 4 | 1u << 14 | swizzle << 29;
 }
 // kind::f16, D fp32, A and B fp16; b_mn: B is MN-major.
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn) {
   return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
-// D[tmem] (+)= A[tmem] * B[smem] of the pair.
-__device__ __forceinline__ void umma_f16_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                                 uint32_t accumulate) {
+// Pair MMAs, operand descriptors by their words: D[tmem] (+)= A[smem] * B[smem], and with A in tensor memory.
+template <uint32_t A_HI, uint32_t B_HI, uint32_t IDESC>
+__device__ __forceinline__ void umma_f16_ss_pair(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %4};\n\tmov.b64 db, {%2, %5};\n\t"
+      "setp.ne.b32 p, %3, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %6, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(accumulate), "n"(A_HI), "n"(B_HI), "r"(IDESC)
+      : "memory");
+}
+template <uint32_t B_HI, uint32_t IDESC>
+__device__ __forceinline__ void umma_f16_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+      "mov.b64 db, {%2, %4};\n\t"
+      "setp.ne.b32 p, %3, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], db, %5, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(accumulate), "n"(B_HI), "r"(IDESC)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -342,7 +346,11 @@ struct TileSoftmax {
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
-      if (lane_id() == 0) mbar_arrive_cluster(p_full);
+      if (lane_id() == 0) {
+        mbar_arrive_remote(p_full);
+        if (j % kMetaBatch == kMetaBatch - 1)
+          mbar_arrive(smem_u32(&bars->meta_empty[j / kMetaBatch % kMetaBatches]));
+      }
     }
     return true;
   }
@@ -383,7 +391,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     abort_flag = 0;
     const uint32_t b = smem_u32(&bars);
     constexpr int kPair = 2 * kMetaBatches, kLocal = kPair + 2 * kTileStages + 2;  // barriers that 8 warps of the pair arrive on
-    for (int i = 0; i < kTileBars; ++i) mbar_init(b + 8 * i, i >= kPair && i < kLocal ? 8 : 1);
+    for (int i = 0; i < kTileBars; ++i)  // meta_empty: the CTA's warps that read the scales
+      mbar_init(b + 8 * i, i < kMetaBatches ? 1 : i < kPair ? 4 * tiles + 4 : i < kLocal ? 8 : 1);
     fence_barrier_init();
   }
   if (warp == 12) {
@@ -446,56 +455,63 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_base;
 
-  auto issue_mmas = [&]() {  // one thread of the first CTA
+  auto issue_mmas = [&]() {  // one thread of the first CTA; what it does between two MMAs delays all
     constexpr uint32_t kIdS = idesc_f16_f32(256, kTileKeys, false), kIdO = idesc_f16_f32(256, D, true);
-    const uint32_t sb = smem_u32(smem);
-    auto scores = [&](int t, int j) {
-      const uint32_t qa = sb + L::q + t * L::kQ, ka = sb + L::k + (j % kTileStages) * L::kHalf;
+    constexpr uint32_t kHiK = desc_hi(1024, 2), kHiV = desc_hi(8 * D, D == 128 ? 2 : 4);
+    const uint32_t q_lo = desc_lo(smem_u32(smem) + L::q), k_lo = desc_lo(smem_u32(smem) + L::k);
+    const uint32_t v_lo = desc_lo(smem_u32(smem) + L::v), bar = smem_u32(&bars);
+    auto at = [&](const void* b) { return bar + static_cast<uint32_t>(static_cast<const char*>(b) - reinterpret_cast<const char*>(&bars)); };
+    auto scores = [&](int t, int st) {
+      const uint32_t qa = q_lo + t * (L::kQ / 16), ka = k_lo + st * (L::kHalf / 16);
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
-        umma_bf16_pair(tmem + 128 * t, sw128_kmajor_desc(qa + (i / 4) * (128 * 128) + (i % 4) * 32),
-                       sw128_kmajor_desc(ka + (i / 4) * (64 * 128) + (i % 4) * 32), kIdS, i > 0);
-      umma_commit_pair(smem_u32(&bars.s_full[t]), 3);
+        umma_f16_ss_pair<kHiK, kHiK, kIdS>(tmem + 128 * t, qa + ((i / 4) * (128 * 128) + (i % 4) * 32) / 16,
+                                           ka + ((i / 4) * (64 * 128) + (i % 4) * 32) / 16, i > 0);
+      umma_commit_pair(at(&bars.s_full[t]), 3);
     };
-    bool ok = mbar_wait_cluster(smem_u32(&bars.k_full[0]), 0, &abort_flag);
+    bool ok = mbar_wait_cluster(at(&bars.k_full[0]), 0, &abort_flag);
     if (ok) {
       tc_fence_after();
-      for (int t = 0; t < tiles; ++t) scores(t, 0);
-      umma_commit_pair(smem_u32(&bars.k_empty[0]), 3);
+      scores(0, 0);
+      if (tiles > 1) scores(1, 0);
+      umma_commit_pair(at(&bars.k_empty[0]), 3);
     }
+    int st = 0, nx = 1 % kTileStages;     // stage of key tile j and of j + 1
+    uint32_t st_par = 0, nx_par = 0, par = 0;
     for (int j = 0; ok && j < n; ++j) {
-      const int st = j % kTileStages, nx = (j + 1) % kTileStages;
-      for (int t = 0; ok && t < tiles; ++t) {
-        ok = mbar_wait_cluster(smem_u32(&bars.v_full[st]), (j / kTileStages) & 1, &abort_flag) &&
-             mbar_wait_cluster(smem_u32(&bars.p_full[t]), j & 1, &abort_flag);
-        if (!ok) break;
+      const bool more = j + 1 < n;
+      ok = mbar_wait_cluster(at(&bars.v_full[0]) + 8 * st, st_par, &abort_flag);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (!ok || t >= tiles) break;
+        // what p_full hands over lies in tensor memory, ordered by the tcgen05 fences around the barrier
+        if (!(ok = mbar_wait(at(&bars.p_full[t]), par, &abort_flag))) break;
         tc_fence_after();
-        const uint32_t va = sb + L::v + st * L::kHalf;
+        const uint32_t va = v_lo + st * (L::kHalf / 16);
 #pragma unroll
         for (int i = 0; i < kTileKeys / 16; ++i)
-          umma_f16_ts_pair(tmem + 256 + D * t, tmem + 128 * t + 8 * i, mnmajor_desc<D / 2>(va + i * (16 * D)), kIdO,
-                           j > 0 || i > 0);
-        if (j + 1 < n) {
-          ok = mbar_wait_cluster(smem_u32(&bars.k_full[nx]), ((j + 1) / kTileStages) & 1, &abort_flag);
-          if (!ok) break;
-          tc_fence_after();
-          scores(t, j + 1);
+          umma_f16_ts_pair<kHiV, kIdO>(tmem + 256 + D * t, tmem + 128 * t + 8 * i, va + i * D, i > 0 ? 1 : j);
+        if (more) {
+          if (t == 0) {
+            if (!(ok = mbar_wait_cluster(at(&bars.k_full[0]) + 8 * nx, nx_par, &abort_flag))) break;
+            tc_fence_after();
+          }
+          scores(t, nx);
         } else {
-          umma_commit_pair(smem_u32(&bars.o_full[t]), 3);
+          umma_commit_pair(at(&bars.o_full[t]), 3);
         }
       }
       if (ok) {
-        umma_commit_pair(smem_u32(&bars.v_empty[st]), 3);
-        if (j + 1 < n) umma_commit_pair(smem_u32(&bars.k_empty[nx]), 3);
-        // p_full of both row tiles and CTAs: nobody reads this key tile's scales any more
-        if (j % kMetaBatch == kMetaBatch - 1)
-          for (int c = 0; c < 2; ++c)
-            mbar_arrive_cluster(mapa_shared(smem_u32(&bars.meta_empty[j / kMetaBatch % kMetaBatches]), c));
+        umma_commit_pair(at(&bars.v_empty[0]) + 8 * st, 3);
+        if (more) umma_commit_pair(at(&bars.k_empty[0]) + 8 * nx, 3);
       }
+      par ^= 1;
+      st = nx, st_par = nx_par;
+      if (++nx == kTileStages) nx = 0, nx_par ^= 1;
     }
     // whatever was issued has finished before shared and tensor memory are given up
-    umma_commit_pair(smem_u32(&bars.drain), 3);
-    mbar_drain(smem_u32(&bars.drain), 0);
+    umma_commit_pair(at(&bars.drain), 3);
+    mbar_drain(at(&bars.drain), 0);
   };
   auto look_up = [&]() {
     for (int b = 0; b * kMetaBatch < n; ++b) {
@@ -514,8 +530,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         }
       }
       const uint32_t there = __ballot_sync(~0u, at >= 0);
-      if (!__all_sync(~0u, mbar_wait_cluster(smem_u32(&bars.meta_empty[b % kMetaBatches]), ((b / kMetaBatches) & 1) ^ 1,
-                                             &abort_flag)))
+      if (!__all_sync(~0u, mbar_wait(smem_u32(&bars.meta_empty[b % kMetaBatches]), ((b / kMetaBatches) & 1) ^ 1,
+                                     &abort_flag)))
         break;
       TileMeta& M = metas[j % kMetaSlots];
       const int c = lane % kTileCells;
@@ -551,7 +567,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         x.template store_v<E4M3>(smem + L::v + st * L::kHalf, last, seq.T, w, lane);
         fence_proxy_async_shared();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&bars.v_full[st]), 0));
+        if (lane == 0) {
+          mbar_arrive_cluster(mapa_shared(smem_u32(&bars.v_full[st]), 0));
+          if ((j - 1) % kMetaBatch == kMetaBatch - 1)
+            mbar_arrive(smem_u32(&bars.meta_empty[(j - 1) / kMetaBatch % kMetaBatches]));
+        }
       }
       if (j < n) x.load_v(vcodes, next, rank, w, lane);
     }
