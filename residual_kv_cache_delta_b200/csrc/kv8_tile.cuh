@@ -11,6 +11,8 @@
 //   warps 8-11      load codes into registers, a key tile ahead, and turn them into fp16 operands in shared memory; K and V,
 //                   which lie alike (rows of keys), are a K-major and an MN-major operand
 //   warp 12         issues the MMAs (first CTA);  warp 13 looks up block ids and scales, four key tiles at a time
+//   warps 14, 15    of the second CTA pass on that its K or V is in place: a release at cluster scope takes about 1000
+//                   clocks, too long for the converters (twice a key tile)
 // The softmax warps take registers from the others (184 against 96 and 48), so that a thread holds its row's 128 scores and
 // tensor memory is read once per key tile.  While one row tile is in its softmax the tensor cores work for the other.
 //
@@ -47,7 +49,8 @@ struct TileSmem {
 
 struct TileBars {
   uint64_t meta_full[kMetaBatches], meta_empty[kMetaBatches];
-  uint64_t k_full[kTileStages], v_full[kTileStages], p_full[2];    // of the pair, in the first CTA: both CTAs arrive
+  uint64_t p_full[2];                                // of the pair, in the first CTA: both CTAs' warps arrive
+  uint64_t k_full[kTileStages], v_full[kTileStages];    // of each CTA's converters; in the first, the second's word too
   uint64_t k_empty[kTileStages], v_empty[kTileStages], s_full[2], o_full[2], drain;  // in both: the MMAs' commits arrive
 };
 constexpr int kTileBars = sizeof(TileBars) / 8;
@@ -390,9 +393,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
   if (threadIdx.x == 0) {
     abort_flag = 0;
     const uint32_t b = smem_u32(&bars);
-    constexpr int kPair = 2 * kMetaBatches, kLocal = kPair + 2 * kTileStages + 2;  // barriers that 8 warps of the pair arrive on
+    constexpr int kP = 2 * kMetaBatches, kFull = kP + 2, kRest = kFull + 2 * kTileStages;
     for (int i = 0; i < kTileBars; ++i)  // meta_empty: the CTA's warps that read the scales
-      mbar_init(b + 8 * i, i < kMetaBatches ? 1 : i < kPair ? 4 * tiles + 4 : i < kLocal ? 8 : 1);
+      mbar_init(b + 8 * i, i < kMetaBatches ? 1 : i < kP ? 4 * tiles + 4 : i < kFull ? 8 : i < kRest ? (rank == 0 ? 5 : 4) : 1);
     fence_barrier_init();
   }
   if (warp == 12) {
@@ -559,7 +562,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         x.template store_k<E4M3>(smem + L::k + st * L::kHalf, w, lane);
         fence_proxy_async_shared();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&bars.k_full[st]), 0));
+        if (lane == 0) mbar_arrive(smem_u32(&bars.k_full[st]));
       }
       if (j < n) x.load_k(a.codes, next, rank, w, lane);
       if (j > 0) {
@@ -568,12 +571,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive_cluster(mapa_shared(smem_u32(&bars.v_full[st]), 0));
+          mbar_arrive(smem_u32(&bars.v_full[st]));
           if ((j - 1) % kMetaBatch == kMetaBatch - 1)
             mbar_arrive(smem_u32(&bars.meta_empty[(j - 1) / kMetaBatch % kMetaBatches]));
         }
       }
       if (j < n) x.load_v(vcodes, next, rank, w, lane);
+    }
+  };
+
+  auto pass_on = [&](uint64_t* full) {  // one thread of the second CTA
+    for (int j = 0; j < n; ++j) {
+      const uint32_t bar = smem_u32(full + j % kTileStages);
+      if (!mbar_wait(bar, (j / kTileStages) & 1, &abort_flag)) break;
+      mbar_arrive_cluster(mapa_shared(bar, 0));
     }
   };
 
@@ -641,6 +652,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
   } else {
     regs_give<48>();
     if (warp == 12 && lane == 0 && rank == 0 && n > 0) issue_mmas();
+    if (warp >= 14 && lane == 0 && rank == 1) pass_on(warp == 14 ? bars.k_full : bars.v_full);
     __syncwarp();
     if (warp == 13) look_up();
   }
