@@ -1,33 +1,39 @@
 // Attention over the 8-bit cache for many query rows (prefill chunks, packed prompts) on tcgen05.
 //
 // A pair of CTAs takes up to 512 rows (a row is a query token and a head of the kv head's group) as two row tiles of 256,
-// 128 of each tile's rows per CTA, and a range of keys in tiles of 128 (eight 16-key cells).  Per key tile and row tile
-//   S = Q K^T (M = 256 rows, N = 128 keys, K = d),   P = 2^(z - m),   O += P V (N = d, K = 128 keys)
-// as pair MMAs (cta_group::2), S and O in tensor memory, P written over S as fp16 and read by the second MMA from
-// there.  Each CTA makes half of the shared operands: 64 keys of K, half of V's dimensions.  With one CTA per tile the
-// shared memory that feeds S (M = N = 128, both operands from there) is the limit: 117 clocks per 128 x 128 x 16 MMA
-// measured against 64 for the pair's 256 x 128 x 16, and every code is converted twice.  Roles in each CTA:
+// 128 of each tile's rows per CTA, and a range of keys in tiles of 64 (four 16-key cells).  Per key tile and row tile
+//   S = Q K^T (M = 256 rows, N = 64 keys, K = d),   P = 2^(z - m),   O += P V (N = d, K = 64 keys)
+// as pair MMAs (cta_group::2) with S, P (fp16) and O in tensor memory.  Each CTA makes half of the shared operands: 32 keys
+// of K, half of V's dimensions.  With one CTA per tile the shared memory that feeds S (M = N = 128, both operands from
+// there) is the limit: 117 clocks per 128 x 128 x 16 MMA measured against 64 for the pair's 256 x 128 x 16, and every
+// code is converted twice.  Roles in each CTA:
 //   warps 0-3, 4-7  softmax of row tile 0 and 1: a thread owns a row (a tensor-memory lane)
-//   warps 8-11      load codes into registers, a key tile ahead, and turn them into fp16 operands in shared memory; K and V,
-//                   which lie alike (rows of keys), are a K-major and an MN-major operand
-//   warp 12         issues the MMAs (first CTA);  warp 13 looks up block ids and scales, four key tiles at a time
+//   warps 8-9, 10-11  load codes of K, of V into registers, three key tiles ahead, and turn them into fp16 operands in shared
+//                   memory; K and V, which lie alike (rows of keys), are a K-major and an MN-major operand
+//   warp 12         issues the MMAs (first CTA);  warp 13 looks up block ids and scales, eight key tiles at a time
 //   warps 14, 15    of the second CTA pass on that its K or V is in place: a release at cluster scope takes about 1000
-//                   clocks, too long for the converters (twice a key tile)
-// The softmax warps take registers from the others (184 against 96 and 48), so that a thread holds its row's 128 scores and
-// tensor memory is read once per key tile.  While one row tile is in its softmax the tensor cores work for the other.
+//                   clocks, too long for the converters
+// Tiles of 64 keys leave tensor memory for P beside S and O.  A thread takes its row's scores out of S at once, so the next
+// key tile's S is made while this one's softmax runs, and P V while the next one's does: the softmax warps, whose exp2
+// (16 a clock and SM) takes as long as the MMAs, wait for neither.  With 128-key tiles, P over S, the chain S, softmax,
+// P V of a row tile took 5400 clocks per 128 keys, of which the MMAs need 2048.
 //
 // Codes are exact in fp16; scales stay out of the operands as in kv8_stream.cuh: the K scale multiplies the fp32 score,
 // the V scale is part of the exponent z = score + log2(v scale), and the sum of weights takes it out again.  The running
 // maximum is raised (and O rescaled in tensor memory) only when a row passes it by more than 2^8.
 #pragma once
 
+#include <cstddef>
+#include <type_traits>
+
 #include "kv8_append.cuh"
 #include "kv8_stream.cuh"
 
 namespace dkv {
 
-constexpr int kTileThreads = 512, kTileRows = 512, kTileKeys = 128, kTileCells = kTileKeys / kKv8CellKeys;
-constexpr int kTileStages = 3;       // of K and of V
+constexpr int kTileThreads = 512, kTileRows = 512, kTileKeys = 64, kTileCells = kTileKeys / kKv8CellKeys;
+constexpr int kTileStages = 4;       // of K and of V
+constexpr int kTileAhead = 3;        // key tiles in a converter's registers
 constexpr float kTileSlack = 8.0f;   // log2 of the most a weight may exceed 1 before the maximum is raised (fp16: 2^16)
 // Key tiles looked up at a time (a lane per cell), and how many such batches are kept.
 constexpr int kMetaBatch = 32 / kTileCells, kMetaBatches = 4, kMetaSlots = kMetaBatch * kMetaBatches;
@@ -49,9 +55,9 @@ struct TileSmem {
 
 struct TileBars {
   uint64_t meta_full[kMetaBatches], meta_empty[kMetaBatches];
-  uint64_t p_full[2];                                // of the pair, in the first CTA: both CTAs' warps arrive
+  uint64_t s_free[2], p_full[2];                     // of the pair, in the first CTA: both CTAs' softmax warps arrive
   uint64_t k_full[kTileStages], v_full[kTileStages];    // of each CTA's converters; in the first, the second's word too
-  uint64_t k_empty[kTileStages], v_empty[kTileStages], s_full[2], o_full[2], drain;  // in both: the MMAs' commits arrive
+  uint64_t k_empty[kTileStages], v_empty[kTileStages], s_full[2], pv_done[2], drain;  // in both: the MMAs' commits arrive
 };
 constexpr int kTileBars = sizeof(TileBars) / 8;
 
@@ -65,25 +71,42 @@ __host__ __device__ constexpr uint32_t desc_hi(uint32_t stride, uint32_t swizzle
 __host__ __device__ constexpr uint32_t idesc_f16_f32(int M, int N, bool b_mn) {
   return (1u << 4) | (b_mn ? 1u << 16 : 0u) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
-// Pair MMAs, operand descriptors by their words: D[tmem] (+)= A[smem] * B[smem], and with A in tensor memory.
+// One lane of a converged warp, always the same.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r;
+}
+// Pair MMAs, operand descriptors by their words: D[tmem] (+)= A[smem] * B[smem], and with A in tensor memory; and the commit
+// to a barrier of both CTAs.  The whole warp executes them and `on` holds for one lane: operands then are uniform registers
+// from the start, where a lone thread's have to be moved there (70 to 90 clocks an MMA measured).
 template <uint32_t A_HI, uint32_t B_HI, uint32_t IDESC>
-__device__ __forceinline__ void umma_f16_ss_pair(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t accumulate) {
+__device__ __forceinline__ void umma_f16_ss_pair(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t accumulate,
+                                                 uint32_t on) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\t"
       "mov.b64 da, {%1, %4};\n\tmov.b64 db, {%2, %5};\n\t"
-      "setp.ne.b32 p, %3, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %6, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_lo), "r"(b_lo), "r"(accumulate), "n"(A_HI), "n"(B_HI), "r"(IDESC)
+      "setp.ne.b32 p, %3, 0;\n\tsetp.ne.b32 q, %7, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], da, db, %6, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(accumulate), "n"(A_HI), "n"(B_HI), "r"(IDESC), "r"(on)
       : "memory");
 }
 template <uint32_t B_HI, uint32_t IDESC>
-__device__ __forceinline__ void umma_f16_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t accumulate) {
+__device__ __forceinline__ void umma_f16_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t accumulate,
+                                                 uint32_t on) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\t"
       "mov.b64 db, {%2, %4};\n\t"
-      "setp.ne.b32 p, %3, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], db, %5, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "r"(b_lo), "r"(accumulate), "n"(B_HI), "r"(IDESC)
+      "setp.ne.b32 p, %3, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], db, %5, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(accumulate), "n"(B_HI), "r"(IDESC), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void umma_commit_both(uint32_t bar, uint32_t on) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %2, 0;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+      "h"(static_cast<uint16_t>(3)), "r"(on)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -139,50 +162,38 @@ __device__ __forceinline__ uint4 load_codes16(const uint8_t* p) {
   return w;
 }
 
-// A converter warp's share of a CTA's half of a key tile, in registers: K rows 64 rank + 16 warp .. + 15, all dimensions; V
-// rows 32 warp .. + 31, dimensions (d / 2) rank .. + d / 2.
-template <int D>
+// A converter warp's share of a key tile in registers.  Of K: 16 rows (one cell) of the CTA's 32 keys, all dimensions; of V: 32
+// of the 64 keys, the CTA's half of the dimensions.
+template <int D, bool V>
 struct TileCodes {
-  static constexpr int kKLanes = D / 16, kKRows = 32 / kKLanes, kVLanes = D / 32, kVRows = 32 / kVLanes;
-  uint4 k[16 / kKRows], v[32 / kVRows];
+  static constexpr int kLanes = V ? D / 32 : D / 16;  // of a row, 16 codes each
+  static constexpr int kRows = 32 / kLanes, kIters = (V ? 32 : 16) / kRows;
+  uint4 w[kIters];
 
-  __device__ __forceinline__ void load_k(const uint8_t* codes, const TileMeta& M, int rank, int warp, int lane) {
-    const int cell = 4 * rank + warp;  // 16 rows of one cell
+  // codes: of the K or V part; M's cell offsets are K's
+  __device__ __forceinline__ void load(const uint8_t* codes, const TileMeta& M, int rank, int sub, int lane) {
 #pragma unroll
-    for (int i = 0; i < 16 / kKRows; ++i) {
-      k[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < kIters; ++i) {
+      const int r = i * kRows + lane / kLanes, cell = V ? 2 * sub + r / kKv8CellKeys : 2 * rank + sub;
+      w[i] = make_uint4(0u, 0u, 0u, 0u);
       if ((M.there >> cell) & 1)
-        k[i] = load_codes16(codes + M.at[cell] + (i * kKRows + lane / kKLanes) * D + (lane % kKLanes) * 16);
+        w[i] = load_codes16(codes + M.at[cell] + (r % kKv8CellKeys) * D + (V ? rank * (D / 2) : 0) + (lane % kLanes) * 16);
     }
   }
-  __device__ __forceinline__ void load_v(const uint8_t* codes, const TileMeta& M, int rank, int warp, int lane) {
-#pragma unroll
-    for (int i = 0; i < 32 / kVRows; ++i) {
-      const int r = 32 * warp + i * kVRows + lane / kVLanes, cell = r / kKv8CellKeys;
-      v[i] = make_uint4(0u, 0u, 0u, 0u);
-      if ((M.there >> cell) & 1)
-        v[i] = load_codes16(codes + M.at[cell] + (r % kKv8CellKeys) * D + rank * (D / 2) + (lane % kVLanes) * 16);
-    }
-  }
+  // V rows of no key, from T on, are stored as 0: weight 0 times them must stay 0, and e4m3 bytes may be NaN.
   template <bool E4M3>
-  __device__ __forceinline__ void store_k(uint8_t* dst, int warp, int lane) const {  // panels of 64 rows of 128 bytes
-    const int c = lane % kKLanes;
+  __device__ __forceinline__ void store(uint8_t* dst, const TileMeta& M, int T, int sub, int lane) const {
+    const int c = lane % kLanes;
 #pragma unroll
-    for (int i = 0; i < 16 / kKRows; ++i) {
-      const int r = 16 * warp + i * kKRows + lane / kKLanes;
-      store_codes<E4M3>(dst + (c / 4) * (64 * 128) + r * 128, (c % 4) * 2, r & 7, c / 4, k[i]);
-    }
-  }
-  // Rows of no key, from T on, are stored as 0: weight 0 times them must stay 0, and e4m3 bytes may be NaN.
-  template <bool E4M3>
-  __device__ __forceinline__ void store_v(uint8_t* dst, const TileMeta& M, int T, int warp, int lane) const {
-    const int c = lane % kVLanes;  // rows of d / 2 fp16: 128 or 64 bytes
-#pragma unroll
-    for (int i = 0; i < 32 / kVRows; ++i) {
-      const int r = 32 * warp + i * kVRows + lane / kVLanes;
-      uint4 x = v[i];
-      if (M.key0[r / kKv8CellKeys] + r % kKv8CellKeys >= T) x = make_uint4(0u, 0u, 0u, 0u);
-      store_codes<E4M3>(dst + r * D, 2 * c, D == 128 ? r & 7 : (r >> 1) & 3, 0, x);
+    for (int i = 0; i < kIters; ++i) {
+      const int r = (V ? 32 : 16) * sub + i * kRows + lane / kLanes;
+      if constexpr (V) {  // rows of d / 2 fp16: 128 or 64 bytes
+        uint4 x = w[i];
+        if (M.key0[r / kKv8CellKeys] + r % kKv8CellKeys >= T) x = make_uint4(0u, 0u, 0u, 0u);
+        store_codes<E4M3>(dst + r * D, 2 * c, D == 128 ? r & 7 : (r >> 1) & 3, 0, x);
+      } else {            // panels of 32 rows of 128 bytes
+        store_codes<E4M3>(dst + (c / 4) * (32 * 128) + r * 128, (c % 4) * 2, r & 7, c / 4, w[i]);
+      }
     }
   }
 };
@@ -195,8 +206,8 @@ struct TileSoftmax {
   const TileMeta* metas;
   TileBars* bars;
   volatile int* abort_flag;
-  uint32_t s_tmem, o_tmem;  // of this warp's lanes
-  uint32_t p_full;          // cluster address of the pair's barrier
+  uint32_t s_tmem, p_tmem, o_tmem;  // of this warp's lanes
+  uint32_t s_free, p_full;          // cluster addresses of the pair's barriers
   int tile;
   Kv8Row row;
   float scl, slope;  // row scale times the softmax scale (natural units); slope in log2 units
@@ -223,16 +234,15 @@ struct TileSoftmax {
     return top;
   }
 
-  // The same where every key is seen and stands at or before the row's position, two columns to an instruction.  Capped
-  // scores: tanh(y) = y P(y^2) with a polynomial (Chebyshev interpolation of degree 4 in y^2 on [0, 0.36], relative error
-  // 7.2e-8), where exp2 and a reciprocal would keep the special-function unit for three times as long as the softmax's own
-  // exp2 does; `most` is raised to the largest y^2, which must stay within 0.36.
-  __device__ __forceinline__ float scores_quick(const TileMeta& M, int cell, uint32_t* r, float& most) {
+  // The same without masks, for keys that stand at or before the row's position (or no distance bias), two columns to an
+  // instruction.  Capped scores: tanh(y) = y P(y^2) with a polynomial (Chebyshev interpolation of degree 4 in y^2 on [0,
+  // 0.36], relative error 7.2e-8), where exp2 and a reciprocal would keep the special-function unit for three times as long
+  // as the softmax's own exp2 does; `most` is raised to the largest y^2, which must stay within 0.36.
+  __device__ __forceinline__ void scores_quick(const TileMeta& M, int cell, uint32_t* r, float per_cap, float& most) {
     const float lv = fmaf(-slope, static_cast<float>(row.pos - M.key0[cell]), M.lv[cell]);
     const bool cap = a.softcap > 0.f;
-    const float kk = cap ? M.ks[cell] * scl / a.softcap : M.ks[cell] * scl * kLog2e, out = a.softcap * kLog2e;
+    const float kk = M.ks[cell] * scl * (cap ? per_cap : kLog2e), out = a.softcap * kLog2e;
     const uint64_t kk2 = pack2(kk, kk), out2 = pack2(out, out), lv2 = pack2(lv, lv), sl2 = pack2(slope, slope);
-    float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < 16; i += 2) {
       uint64_t y = mul2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), kk2);
@@ -250,13 +260,24 @@ struct TileSoftmax {
       y = add2(y, fma2(sl2, pack2(static_cast<float>(i), static_cast<float>(i + 1)), lv2));
       unpack2(y, x0, x1);
       r[i] = __float_as_uint(x0), r[i + 1] = __float_as_uint(x1);
-      top = fmaxf(fmaxf(top, x0), x1);
     }
-    return top;
+  }
+
+  __device__ __forceinline__ void load_scores(uint32_t (&r)[2][32]) {
+    tmem_ld_32x32b_x32(s_tmem, r[0]);
+    tmem_ld_32x32b_x32(s_tmem + 32, r[1]);
+    tmem_ld_wait();
+  }
+  __device__ __forceinline__ void free_scores() {  // S may be written again
+    tc_fence_before();
+    __syncwarp();
+    if (lane_id() == 0) mbar_arrive_remote(s_free);
   }
 
   __device__ __forceinline__ bool run(int n) {
     const float two_over_cap = BIAS && a.softcap > 0.f ? 2.0f * kLog2e / a.softcap : 0.f;
+    const float per_cap = BIAS && a.softcap > 0.f ? 1.0f / a.softcap : 0.f;
+    const bool behind = BIAS && __all_sync(~0u, slope == 0.f || seq.prefix <= row.pos + 1);
     for (int j = 0; j < n; ++j) {
       bool ok = true;
       if (j % kMetaBatch == 0)
@@ -264,52 +285,71 @@ struct TileSoftmax {
       if (!__all_sync(~0u, ok && mbar_wait(smem_u32(&bars->s_full[tile]), j & 1, abort_flag))) return false;
       tc_fence_after();
       const TileMeta& M = metas[j % kMetaSlots];
-      uint32_t r[4][32];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(s_tmem + 32 * c, r[c]);
+      uint32_t r[2][32];
+      load_scores(r);
+      if (!BIAS) free_scores();
       const int k0 = M.key0[0], k1 = M.key0[kTileCells - 1] + kKv8CellKeys - 1;
-      // quick: every key of the tile is seen by all of the warp's rows and, without a bias, z is one fused multiply-add of
-      // the raw score, done again in the second pass.  m then is not the exact maximum of those sums, but
-      // within a rounding of it, so scores whose rounding is not small against 1 take the other path.
-      bool quick = __all_sync(~0u, M.there == (1 << kTileCells) - 1 && k1 - k0 == kTileKeys - 1 && row.lo <= k0 &&
-                                       k1 <= row.hi);
+      // whole: every key of the tile is seen by all of the warp's rows
+      const bool whole = __all_sync(~0u, M.there == (1 << kTileCells) - 1 && k1 - k0 == kTileKeys - 1 && row.lo <= k0 &&
+                                             k1 <= row.hi);
+      // raw: without a bias z is one fused multiply-add of the raw score, done again in the second pass.  m then is not
+      // the exact maximum of those sums, but within a rounding of it, so scores whose rounding is not small against 1 take
+      // the other path.
+      bool raw = !BIAS && whole;
       float top = -INFINITY;
-      tmem_ld_wait();
-      if (quick && BIAS) {
+      if (BIAS) {
         float most = 0.f;
+        if (behind)
 #pragma unroll
-        for (int cell = 0; cell < kTileCells; ++cell)
-          top = fmaxf(top, scores_quick(M, cell, &r[cell / 2][16 * (cell % 2)], most));
-        quick = __all_sync(~0u, most <= 0.36f);
-        if (!quick) {
+          for (int cell = 0; cell < kTileCells; ++cell)
+            scores_quick(M, cell, &r[cell / 2][16 * (cell % 2)], per_cap, most);
+        if (__all_sync(~0u, behind && most <= 0.36f)) {
+          if (!whole)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(s_tmem + 32 * c, r[c]);
-          tmem_ld_wait();
+            for (int cell = 0; cell < kTileCells; ++cell) {
+              const uint32_t bits = (M.there >> cell) & 1 ? cell_bits(row, seq.prefix, M.key0[cell]) : 0u;
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (!((bits >> i) & 1u)) r[cell / 2][16 * (cell % 2) + i] = 0xff800000u;
+            }
+#pragma unroll
+          for (int i = 0; i < 64; i += 2)
+            top = fmaxf(fmaxf(top, __uint_as_float(r[i / 32][i % 32])), __uint_as_float(r[i / 32][i % 32 + 1]));
+        } else {
+          load_scores(r);
+#pragma unroll
+          for (int cell = 0; cell < kTileCells; ++cell)
+            top = fmaxf(top, scores(M, cell, &r[cell / 2][16 * (cell % 2)], two_over_cap));
         }
-      } else if (quick) {
+        free_scores();
+      } else {
+        if (raw) {
 #pragma unroll
-        for (int cell = 0; cell < kTileCells; ++cell) {
-          const uint32_t* x = &r[cell / 2][16 * (cell % 2)];
-          float y = __uint_as_float(x[0]);
+          for (int cell = 0; cell < kTileCells; ++cell) {
+            const uint32_t* x = &r[cell / 2][16 * (cell % 2)];
+            float y = __uint_as_float(x[0]);
 #pragma unroll
-          for (int i = 1; i < 15; i += 2) y = fmaxf(fmaxf(y, __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
-          y = fmaxf(y, __uint_as_float(x[15]));
-          top = fmaxf(top, fmaf(y, M.ks[cell] * scl * kLog2e, M.lv[cell]));
+            for (int i = 1; i < 15; i += 2) y = fmaxf(fmaxf(y, __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
+            y = fmaxf(y, __uint_as_float(x[15]));
+            top = fmaxf(top, fmaf(y, M.ks[cell] * scl * kLog2e, M.lv[cell]));
+          }
+          raw = __all_sync(~0u, fabsf(top) < 65536.0f);
         }
-        quick = __all_sync(~0u, fabsf(top) < 65536.0f);
-      }
-      if (!quick) {
-        top = -INFINITY;
+        if (!raw) {
+          top = -INFINITY;
 #pragma unroll
-        for (int cell = 0; cell < kTileCells; ++cell)
-          top = fmaxf(top, scores(M, cell, &r[cell / 2][16 * (cell % 2)], two_over_cap));
+          for (int cell = 0; cell < kTileCells; ++cell)
+            top = fmaxf(top, scores(M, cell, &r[cell / 2][16 * (cell % 2)], two_over_cap));
+        }
       }
-      const bool rise = top > m + kTileSlack;
-      if (__any_sync(~0u, rise)) {
+      const bool rise = top > m + kTileSlack, any = __any_sync(~0u, rise);
+      if (any) {
         const float now = rise ? top : m, fix = fast_exp2(m - now);
         m = now;
         l *= fix;
         if (j > 0) {
+          if (!__all_sync(~0u, mbar_wait(smem_u32(&bars->pv_done[tile]), (j - 1) & 1, abort_flag))) return false;
+          tc_fence_after();
 #pragma unroll 1
           for (int c = 0; c < D / 16; ++c) {
             uint32_t x[16];
@@ -321,31 +361,30 @@ struct TileSoftmax {
           }
         }
       }
-      const bool raw = quick && !BIAS;  // r still holds the raw scores
+      uint32_t p[2][16];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t p[16];
+      for (int cell = 0; cell < kTileCells; ++cell) {
+        const float kk = raw ? M.ks[cell] * scl * kLog2e : 1.0f, add = raw ? M.lv[cell] - m : -m;
+        const uint64_t kk2 = pack2(kk, kk), add_2 = pack2(add, add);
+        uint64_t sum2 = 0;
+        float x, y;
 #pragma unroll
-        for (int gq = 0; gq < 2; ++gq) {
-          const int cell = 2 * c + gq;
-          const float kk = raw ? M.ks[cell] * scl * kLog2e : 1.0f, add = raw ? M.lv[cell] - m : -m;
-          const uint64_t kk2 = pack2(kk, kk), add_2 = pack2(add, add);
-          uint64_t sum2 = 0;
-#pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            float x, y;
-            unpack2(fma2(pack2(__uint_as_float(r[c][gq * 16 + i]), __uint_as_float(r[c][gq * 16 + i + 1])), kk2, add_2), x, y);
-            x = fast_exp2(x), y = fast_exp2(y);
-            sum2 = add2(sum2, pack2(x, y));
-            p[gq * 8 + i / 2] = pack_f16(x, y);
-          }
-          float x, y;
-          unpack2(sum2, x, y);
-          x += y;
-          if (x != 0.f) l = fmaf(x, M.iv[cell], l);  // a cell out of sight adds nothing, even where its scale is NaN
+        for (int i = 0; i < 16; i += 2) {
+          const uint32_t* q = &r[cell / 2][16 * (cell % 2) + i];
+          unpack2(fma2(pack2(__uint_as_float(q[0]), __uint_as_float(q[1])), kk2, add_2), x, y);
+          x = fast_exp2(x), y = fast_exp2(y);
+          sum2 = add2(sum2, pack2(x, y));
+          p[cell / 2][8 * (cell % 2) + i / 2] = pack_f16(x, y);
         }
-        tmem_st_32x32b_x16(s_tmem + 16 * c, p);
+        unpack2(sum2, x, y);
+        x += y;
+        if (x != 0.f) l = fmaf(x, M.iv[cell], l);  // a cell out of sight adds nothing, even where its scale is NaN
       }
+      // the MMAs have read the last key tile's P
+      if (j > 0 && !__all_sync(~0u, mbar_wait(smem_u32(&bars->pv_done[tile]), (j - 1) & 1, abort_flag))) return false;
+      tc_fence_after();
+      tmem_st_32x32b_x16(p_tmem, p[0]);
+      tmem_st_32x32b_x16(p_tmem + 16, p[1]);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -393,9 +432,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
   if (threadIdx.x == 0) {
     abort_flag = 0;
     const uint32_t b = smem_u32(&bars);
-    constexpr int kP = 2 * kMetaBatches, kFull = kP + 2, kRest = kFull + 2 * kTileStages;
-    for (int i = 0; i < kTileBars; ++i)  // meta_empty: the CTA's warps that read the scales
-      mbar_init(b + 8 * i, i < kMetaBatches ? 1 : i < kP ? 4 * tiles + 4 : i < kFull ? 8 : i < kRest ? (rank == 0 ? 5 : 4) : 1);
+    constexpr int kP = 2 * kMetaBatches, kFull = kP + 4, kRest = kFull + 2 * kTileStages;
+    for (int i = 0; i < kTileBars; ++i)  // meta_empty: the CTA's warps that read a batch
+      mbar_init(b + 8 * i, i < kMetaBatches ? 1 : i < kP ? 4 * tiles + 4 : i < kFull ? 8 : i < kRest ? (rank == 0 ? 3 : 2) : 1);
     fence_barrier_init();
   }
   if (warp == 12) {
@@ -458,67 +497,76 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_base;
 
-  auto issue_mmas = [&]() {  // one thread of the first CTA; what it does between two MMAs delays all
+  auto issue_mmas = [&]() {  // one warp of the first CTA; what it does between two MMAs delays all
     constexpr uint32_t kIdS = idesc_f16_f32(256, kTileKeys, false), kIdO = idesc_f16_f32(256, D, true);
     constexpr uint32_t kHiK = desc_hi(1024, 2), kHiV = desc_hi(8 * D, D == 128 ? 2 : 4);
-    const uint32_t q_lo = desc_lo(smem_u32(smem) + L::q), k_lo = desc_lo(smem_u32(smem) + L::k);
-    const uint32_t v_lo = desc_lo(smem_u32(smem) + L::v), bar = smem_u32(&bars);
-    auto at = [&](const void* b) { return bar + static_cast<uint32_t>(static_cast<const char*>(b) - reinterpret_cast<const char*>(&bars)); };
+    const uint32_t on = elect_one();
+    auto same = [](uint32_t x) { return __shfl_sync(~0u, x, 0); };  // known to the compiler to be uniform
+    const uint32_t sb = same(smem_u32(smem)), bar = same(smem_u32(&bars)), tm = same(tmem);
+    const int num = static_cast<int>(same(n)), num_t = static_cast<int>(same(tiles));
+    const uint32_t q_lo = desc_lo(sb + L::q), k_lo = desc_lo(sb + L::k), v_lo = desc_lo(sb + L::v);
+    constexpr uint32_t kKFull = offsetof(TileBars, k_full), kVFull = offsetof(TileBars, v_full),
+                       kKEmpty = offsetof(TileBars, k_empty), kVEmpty = offsetof(TileBars, v_empty),
+                       kSFree = offsetof(TileBars, s_free), kPFull = offsetof(TileBars, p_full),
+                       kSFull = offsetof(TileBars, s_full), kPvDone = offsetof(TileBars, pv_done),
+                       kDrain = offsetof(TileBars, drain);
+    auto wait_pair = [&](uint32_t b, uint32_t par) { return __all_sync(~0u, mbar_wait_cluster(b, par, &abort_flag)) != 0; };
+    auto wait = [&](uint32_t b, uint32_t par) { return __all_sync(~0u, mbar_wait(b, par, &abort_flag)) != 0; };
     auto scores = [&](int t, int st) {
       const uint32_t qa = q_lo + t * (L::kQ / 16), ka = k_lo + st * (L::kHalf / 16);
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
-        umma_f16_ss_pair<kHiK, kHiK, kIdS>(tmem + 128 * t, qa + ((i / 4) * (128 * 128) + (i % 4) * 32) / 16,
-                                           ka + ((i / 4) * (64 * 128) + (i % 4) * 32) / 16, i > 0);
-      umma_commit_pair(at(&bars.s_full[t]), 3);
+        umma_f16_ss_pair<kHiK, kHiK, kIdS>(tm + kTileKeys * t, qa + ((i / 4) * (128 * 128) + (i % 4) * 32) / 16,
+                                           ka + ((i / 4) * (32 * 128) + (i % 4) * 32) / 16, i > 0, on);
+      umma_commit_both(bar + kSFull + 8 * t, on);
     };
-    bool ok = mbar_wait_cluster(at(&bars.k_full[0]), 0, &abort_flag);
+    bool ok = wait_pair(bar + kKFull, 0);
     if (ok) {
       tc_fence_after();
       scores(0, 0);
-      if (tiles > 1) scores(1, 0);
-      umma_commit_pair(at(&bars.k_empty[0]), 3);
+      if (num_t > 1) scores(1, 0);
+      umma_commit_both(bar + kKEmpty, on);
     }
     int st = 0, nx = 1 % kTileStages;     // stage of key tile j and of j + 1
     uint32_t st_par = 0, nx_par = 0, par = 0;
-    for (int j = 0; ok && j < n; ++j) {
-      const bool more = j + 1 < n;
-      ok = mbar_wait_cluster(at(&bars.v_full[0]) + 8 * st, st_par, &abort_flag);
+    // what s_free and p_full hand over lies in tensor memory, ordered by the tcgen05 fences around the barriers
+    for (int j = 0; ok && j < num; ++j) {
+      if (j + 1 < num) {
+        ok = wait_pair(bar + kKFull + 8 * nx, nx_par);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          if (!ok || t >= num_t) break;
+          if (!(ok = wait(bar + kSFree + 8 * t, par))) break;
+          tc_fence_after();
+          scores(t, nx);
+        }
+        if (!ok) break;
+        umma_commit_both(bar + kKEmpty + 8 * nx, on);
+      }
+      ok = wait_pair(bar + kVFull + 8 * st, st_par);
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        if (!ok || t >= tiles) break;
-        // what p_full hands over lies in tensor memory, ordered by the tcgen05 fences around the barrier
-        if (!(ok = mbar_wait(at(&bars.p_full[t]), par, &abort_flag))) break;
+        if (!ok || t >= num_t) break;
+        if (!(ok = wait(bar + kPFull + 8 * t, par))) break;
         tc_fence_after();
         const uint32_t va = v_lo + st * (L::kHalf / 16);
 #pragma unroll
         for (int i = 0; i < kTileKeys / 16; ++i)
-          umma_f16_ts_pair<kHiV, kIdO>(tmem + 256 + D * t, tmem + 128 * t + 8 * i, va + i * D, i > 0 ? 1 : j);
-        if (more) {
-          if (t == 0) {
-            if (!(ok = mbar_wait_cluster(at(&bars.k_full[0]) + 8 * nx, nx_par, &abort_flag))) break;
-            tc_fence_after();
-          }
-          scores(t, nx);
-        } else {
-          umma_commit_pair(at(&bars.o_full[t]), 3);
-        }
+          umma_f16_ts_pair<kHiV, kIdO>(tm + 256 + D * t, tm + 128 + 32 * t + 8 * i, va + i * D, i > 0 ? 1 : j, on);
+        umma_commit_both(bar + kPvDone + 8 * t, on);
       }
-      if (ok) {
-        umma_commit_pair(at(&bars.v_empty[0]) + 8 * st, 3);
-        if (more) umma_commit_pair(at(&bars.k_empty[0]) + 8 * nx, 3);
-      }
+      if (ok) umma_commit_both(bar + kVEmpty + 8 * st, on);
       par ^= 1;
       st = nx, st_par = nx_par;
       if (++nx == kTileStages) nx = 0, nx_par ^= 1;
     }
     // whatever was issued has finished before shared and tensor memory are given up
-    umma_commit_pair(at(&bars.drain), 3);
-    mbar_drain(at(&bars.drain), 0);
+    umma_commit_both(bar + kDrain, on);
+    mbar_drain(bar + kDrain, 0);
   };
   auto look_up = [&]() {
     for (int b = 0; b * kMetaBatch < n; ++b) {
-      // lane: cell lane % 8 of key tile 4 b + lane / 8; tiles go from the nearest keys to the farthest
+      // a lane per cell; tiles go from the nearest keys to the farthest
       const int j = b * kMetaBatch + lane / kTileCells, v = v0 + (n - 1 - j) * kTileCells + lane % kTileCells;
       int key0 = INT_MAX / 2;
       int64_t at = -1;
@@ -545,41 +593,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
       if (lane == 0) mbar_arrive(smem_u32(&bars.meta_full[b % kMetaBatches]));
     }
   };
-  auto convert = [&]() {
-    TileCodes<D> x;
-    const int w = warp - 8;
-    const uint8_t* vcodes = a.codes + static_cast<int64_t>(a.block) * D;
-    for (int j = 0; j <= n; ++j) {  // stores key tile j - 1, loads j
-      if (j < n && j % kMetaBatch == 0 &&
-          !__all_sync(~0u, mbar_wait(smem_u32(&bars.meta_full[j / kMetaBatch % kMetaBatches]),
-                                     (j / kMetaSlots) & 1, &abort_flag)))
-        break;
-      const TileMeta &last = metas[(j + kMetaSlots - 1) % kMetaSlots], &next = metas[j % kMetaSlots];
-      const int st = (j + kTileStages - 1) % kTileStages;
-      const uint32_t free_par = (((j - 1) / kTileStages) & 1) ^ 1;
-      if (j > 0) {
-        if (!__all_sync(~0u, mbar_wait(smem_u32(&bars.k_empty[st]), free_par, &abort_flag))) break;
-        x.template store_k<E4M3>(smem + L::k + st * L::kHalf, w, lane);
-        fence_proxy_async_shared();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&bars.k_full[st]));
-      }
-      if (j < n) x.load_k(a.codes, next, rank, w, lane);
-      if (j > 0) {
-        if (!__all_sync(~0u, mbar_wait(smem_u32(&bars.v_empty[st]), free_par, &abort_flag))) break;
-        x.template store_v<E4M3>(smem + L::v + st * L::kHalf, last, seq.T, w, lane);
+  // K or V: `sub` is the warp's number among the two
+  auto convert = [&](auto part, uint32_t smem_at, uint64_t* full, uint64_t* empty, int sub) {
+    constexpr bool V = decltype(part)::value;
+    TileCodes<D, V> x[kTileAhead];
+    const uint8_t* codes = a.codes + (V ? static_cast<int64_t>(a.block) * D : 0);
+    bool ok = true;
+    auto load = [&](int j, TileCodes<D, V>& c) {
+      if (j % kMetaBatch == 0)
+        ok = ok && __all_sync(~0u, mbar_wait(smem_u32(&bars.meta_full[j / kMetaBatch % kMetaBatches]),
+                                             (j / kMetaSlots) & 1, &abort_flag));
+      if (ok) c.load(codes, metas[j % kMetaSlots], rank, sub, lane);
+    };
+#pragma unroll
+    for (int i = 0; i < kTileAhead; ++i)
+      if (i < n) load(i, x[i]);
+    int st = 0;
+    uint32_t par = 1;
+    for (int j = 0; ok && j < n; j += kTileAhead) {
+#pragma unroll
+      for (int i = 0; i < kTileAhead; ++i) {
+        if (!ok || j + i >= n) break;
+        if (!(ok = __all_sync(~0u, mbar_wait(smem_u32(empty + st), par, &abort_flag)))) break;
+        x[i].template store<E4M3>(smem + smem_at + st * L::kHalf, metas[(j + i) % kMetaSlots], seq.T, sub, lane);
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(smem_u32(&bars.v_full[st]));
-          if ((j - 1) % kMetaBatch == kMetaBatch - 1)
-            mbar_arrive(smem_u32(&bars.meta_empty[(j - 1) / kMetaBatch % kMetaBatches]));
+          mbar_arrive(smem_u32(full + st));
+          if ((j + i) % kMetaBatch == kMetaBatch - 1)
+            mbar_arrive(smem_u32(&bars.meta_empty[(j + i) / kMetaBatch % kMetaBatches]));
         }
+        if (++st == kTileStages) st = 0, par ^= 1;
+        if (j + i + kTileAhead < n) load(j + i + kTileAhead, x[i]);
       }
-      if (j < n) x.load_v(vcodes, next, rank, w, lane);
     }
   };
-
   auto pass_on = [&](uint64_t* full) {  // one thread of the second CTA
     for (int j = 0; j < n; ++j) {
       const uint32_t bar = smem_u32(full + j % kTileStages);
@@ -588,20 +636,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     }
   };
 
-  // per sub-partition: 2 x 184 + 96 + 48 = 4 x 128 registers a thread, what the CTA was launched with
+  // per sub-partition: 2 x 160 + 136 + 56 = 4 x 128 registers a thread, what the CTA was launched with
   if (warp < 8) {
-    regs_take<184>();
+    regs_take<160>();
     const int tile = warp / 4;
     if (tile < tiles) {
       const uint32_t lanes = static_cast<uint32_t>(warp % 4) << 21;  // (32 * quarter) << 16
       const int r = tile * 128 + (warp % 4) * 32 + lane, rr = min(global_row(r), r1 - 1);
       const bool mine = global_row(r) < r1;
-      TileSoftmax<D, BIAS> sm{a, seq, metas, &bars, &abort_flag, (tmem + 128 * tile) | lanes,
-                              (tmem + 256 + D * tile) | lanes, mapa_shared(smem_u32(&bars.p_full[tile]), 0), tile,
+      TileSoftmax<D, BIAS> sm{a, seq, metas, &bars, &abort_flag, (tmem + 64 * tile) | lanes,
+                              (tmem + 128 + 32 * tile) | lanes, (tmem + 256 + D * tile) | lanes,
+                              mapa_shared(smem_u32(&bars.s_free[tile]), 0), mapa_shared(smem_u32(&bars.p_full[tile]), 0), tile,
                               kv8_row(a, seq, rr / a.group), mine ? qscale[r] : 0.f,
                               a.slopes ? a.slopes[h * a.group + rr % a.group] * kLog2e : 0.f, kNoMax, 0.f};
       bool ok = sm.run(n);
-      if (ok && n > 0) ok = __all_sync(~0u, mbar_wait(smem_u32(&bars.o_full[tile]), 0, &abort_flag));
+      if (ok && n > 0) ok = __all_sync(~0u, mbar_wait(smem_u32(&bars.pv_done[tile]), (n - 1) & 1, &abort_flag));
       tc_fence_after();
       const float sum = ok ? sm.l : NAN;
       const float inv = a.nsplit > 1 ? 1.0f : (sum == 0.f ? 0.f : 1.0f / sum);
@@ -647,11 +696,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
       tc_fence_before();
     }
   } else if (warp < 12) {
-    regs_give<96>();
-    convert();
+    regs_take<136>();
+    if (warp < 10) convert(std::false_type(), L::k, bars.k_full, bars.k_empty, warp - 8);
+    else convert(std::true_type(), L::v, bars.v_full, bars.v_empty, warp - 10);
   } else {
-    regs_give<48>();
-    if (warp == 12 && lane == 0 && rank == 0 && n > 0) issue_mmas();
+    regs_give<56>();
+    if (warp == 12 && rank == 0 && n > 0) issue_mmas();
     if (warp >= 14 && lane == 0 && rank == 1) pass_on(warp == 14 ? bars.k_full : bars.v_full);
     __syncwarp();
     if (warp == 13) look_up();
