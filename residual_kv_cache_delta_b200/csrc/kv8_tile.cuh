@@ -8,15 +8,17 @@
 // there) is the limit: 117 clocks per 128 x 128 x 16 MMA measured against 64 for the pair's 256 x 128 x 16, and every
 // code is converted twice.  Roles in each CTA:
 //   warps 0-3, 4-7  softmax of row tile 0 and 1: a thread owns a row (a tensor-memory lane)
-//   warps 8-9, 10-11  load codes of K, of V into registers, three key tiles ahead, and turn them into fp16 operands in shared
+//   warps 8-9, 10-11  load codes of K, of V into registers, two key tiles ahead, and turn them into fp16 operands in shared
 //                   memory; K and V, which lie alike (rows of keys), are a K-major and an MN-major operand
 //   warp 12         issues the MMAs (first CTA);  warp 13 looks up block ids and scales, eight key tiles at a time
 //   warps 14, 15    of the second CTA pass on that its K or V is in place: a release at cluster scope takes about 1000
 //                   clocks, too long for the converters
-// Tiles of 64 keys leave tensor memory for P beside S and O.  A thread takes its row's scores out of S at once, so the next
-// key tile's S is made while this one's softmax runs, and P V while the next one's does: the softmax warps, whose exp2
-// (16 a clock and SM) takes as long as the MMAs, wait for neither.  With 128-key tiles, P over S, the chain S, softmax,
-// P V of a row tile took 5400 clocks per 128 keys, of which the MMAs need 2048.
+// Tiles of 64 keys leave tensor memory for two S buffers per row tile beside O: a tile's S is made while the softmax of the
+// one before it runs, and P is written over the columns of S that it came from, so that the softmax warps, whose exp2 (16 a
+// clock and SM) takes as long as the MMAs, do not wait for S.  (128-key tiles with one S buffer: the chain S, softmax, P V
+// of a row tile took 5400 clocks per 128 keys, of which the MMAs need 2048.)  The softmax goes through a tile's scores twice
+// in tensor memory, 32 at a time by loops: held in registers with unrolled code, the warps' different programs evicted
+// each other from the instruction caches.
 //
 // Codes are exact in fp16; scales stay out of the operands as in kv8_stream.cuh: the K scale multiplies the fp32 score,
 // the V scale is part of the exponent z = score + log2(v scale), and the sum of weights takes it out again.  The running
@@ -33,16 +35,16 @@ namespace dkv {
 
 constexpr int kTileThreads = 512, kTileRows = 512, kTileKeys = 64, kTileCells = kTileKeys / kKv8CellKeys;
 constexpr int kTileStages = 4;       // of K and of V
-constexpr int kTileAhead = 3;        // key tiles in a converter's registers
+constexpr int kTileAhead = 2;        // key tiles in a converter's registers
 constexpr float kTileSlack = 8.0f;   // log2 of the most a weight may exceed 1 before the maximum is raised (fp16: 2^16)
 // Key tiles looked up at a time (a lane per cell), and how many such batches are kept.
 constexpr int kMetaBatch = 32 / kTileCells, kMetaBatches = 4, kMetaSlots = kMetaBatch * kMetaBatches;
 
-struct TileMeta {  // of one key tile
+struct __align__(16) TileMeta {  // of one key tile
   int64_t at[kTileCells];  // byte offset of a cell's K codes
   int key0[kTileCells];    // its first key
   float ks[kTileCells], lv[kTileCells], iv[kTileCells];  // K scale, log2 and inverse of the V scale
-  int there, pad[3];       // cells that are mapped
+  int there, last, pad[2];  // cells that are mapped; the last key, INT_MAX where the cells are not 64 mapped keys in a row
 };
 
 // Bytes of a CTA's shared memory: 256 rows of Q, its halves of K and V as fp16.
@@ -55,9 +57,11 @@ struct TileSmem {
 
 struct TileBars {
   uint64_t meta_full[kMetaBatches], meta_empty[kMetaBatches];
-  uint64_t s_free[2], p_full[2];                     // of the pair, in the first CTA: both CTAs' softmax warps arrive
+  // per row tile and S buffer, since S and the softmax may be two key tiles ahead of who waits for them:
+  uint64_t p_full[2][2];                             // of the pair, in the first CTA: both CTAs' softmax warps arrive
   uint64_t k_full[kTileStages], v_full[kTileStages];    // of each CTA's converters; in the first, the second's word too
-  uint64_t k_empty[kTileStages], v_empty[kTileStages], s_full[2], pv_done[2], drain;  // in both: the MMAs' commits arrive
+  uint64_t k_empty[kTileStages], v_empty[kTileStages], pv_done[2], drain;  // in both: the MMAs' commits arrive
+  uint64_t s_full[2][2];                             // in both
 };
 constexpr int kTileBars = sizeof(TileBars) / 8;
 
@@ -206,39 +210,31 @@ struct TileSoftmax {
   const TileMeta* metas;
   TileBars* bars;
   volatile int* abort_flag;
-  uint32_t s_tmem, p_tmem, o_tmem;  // of this warp's lanes
-  uint32_t s_free, p_full;          // cluster addresses of the pair's barriers
+  uint32_t s_tmem, o_tmem;  // of this warp's lanes: the first S buffer, O
+  uint32_t p_full;          // cluster address of the pair's barrier of the first S buffer
   int tile;
   Kv8Row row;
   float scl, slope;  // row scale times the softmax scale (natural units); slope in log2 units
   float m, l;
 
-  // The scores of cell `cell` (16 columns) as z, in place; returns their maximum.
-  __device__ __forceinline__ float scores(const TileMeta& M, int cell, uint32_t* r, float two_over_cap) {
-    float top = -INFINITY;
-    const int key0 = M.key0[cell];
-    const float kk = M.ks[cell] * scl, lv = M.lv[cell];
-    uint32_t bits = cell_bits(row, seq.prefix, key0);
-    if (!((M.there >> cell) & 1)) bits = 0;
-    const float gap = static_cast<float>(row.pos - key0);
+  // The scores of cell `cell` (16 columns) as z, in place.
+  __device__ __forceinline__ void scores(const TileMeta& M, int cell, uint32_t (&r)[16], float two_over_cap) {
+    const float kk = M.ks[cell] * scl, lv = M.lv[cell], gap = static_cast<float>(row.pos - M.key0[cell]);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       float x = __uint_as_float(r[i]) * kk;
       if (BIAS && a.softcap > 0.f) x = kv8_cap(x, a.softcap, two_over_cap);
       x = fmaf(x, kLog2e, lv);
       if (BIAS) x = fmaf(-slope, fabsf(gap - static_cast<float>(i)), x);
-      if (!((bits >> i) & 1u)) x = -INFINITY;
       r[i] = __float_as_uint(x);
-      top = fmaxf(top, x);
     }
-    return top;
   }
 
   // The same without masks, for keys that stand at or before the row's position (or no distance bias), two columns to an
   // instruction.  Capped scores: tanh(y) = y P(y^2) with a polynomial (Chebyshev interpolation of degree 4 in y^2 on [0,
   // 0.36], relative error 7.2e-8), where exp2 and a reciprocal would keep the special-function unit for three times as long
   // as the softmax's own exp2 does; `most` is raised to the largest y^2, which must stay within 0.36.
-  __device__ __forceinline__ void scores_quick(const TileMeta& M, int cell, uint32_t* r, float per_cap, float& most) {
+  __device__ __forceinline__ void scores_quick(const TileMeta& M, int cell, uint32_t (&r)[16], float per_cap, float& most) {
     const float lv = fmaf(-slope, static_cast<float>(row.pos - M.key0[cell]), M.lv[cell]);
     const bool cap = a.softcap > 0.f;
     const float kk = M.ks[cell] * scl * (cap ? per_cap : kLog2e), out = a.softcap * kLog2e;
@@ -263,84 +259,81 @@ struct TileSoftmax {
     }
   }
 
-  __device__ __forceinline__ void load_scores(uint32_t (&r)[2][32]) {
-    tmem_ld_32x32b_x32(s_tmem, r[0]);
-    tmem_ld_32x32b_x32(s_tmem + 32, r[1]);
-    tmem_ld_wait();
-  }
-  __device__ __forceinline__ void free_scores() {  // S may be written again
-    tc_fence_before();
-    __syncwarp();
-    if (lane_id() == 0) mbar_arrive_remote(s_free);
+  // The tile's scores in tensor memory as z, masked unless `whole`; returns the row's maximum.
+  __device__ __forceinline__ float transform(const TileMeta& M, uint32_t s_tmem, bool whole, bool behind, float two_over_cap, float per_cap) {
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int cell = 0; cell < kTileCells; ++cell) {
+      uint32_t r[16];
+      tmem_ld_32x32b_x16(s_tmem + 16 * cell, r);
+      tmem_ld_wait();
+      bool quick = BIAS && behind;
+      if (quick) {
+        float most = 0.f;
+        scores_quick(M, cell, r, per_cap, most);
+        quick = __all_sync(~0u, most <= 0.36f);
+        if (!quick) {
+          tmem_ld_32x32b_x16(s_tmem + 16 * cell, r);
+          tmem_ld_wait();
+        }
+      }
+      if (!quick) scores(M, cell, r, two_over_cap);
+      if (!whole) {
+        const uint32_t bits = (M.there >> cell) & 1 ? cell_bits(row, seq.prefix, M.key0[cell]) : 0u;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          if (!((bits >> i) & 1u)) r[i] = 0xff800000u;
+      }
+#pragma unroll
+      for (int i = 0; i < 16; i += 2) top = fmaxf(fmaxf(top, __uint_as_float(r[i])), __uint_as_float(r[i + 1]));
+      tmem_st_32x32b_x16(s_tmem + 16 * cell, r);
+    }
+    tmem_st_wait();
+    return top;
   }
 
   __device__ __forceinline__ bool run(int n) {
     const float two_over_cap = BIAS && a.softcap > 0.f ? 2.0f * kLog2e / a.softcap : 0.f;
     const float per_cap = BIAS && a.softcap > 0.f ? 1.0f / a.softcap : 0.f;
+    const float scl2 = scl * kLog2e;
     const bool behind = BIAS && __all_sync(~0u, slope == 0.f || seq.prefix <= row.pos + 1);
     for (int j = 0; j < n; ++j) {
       bool ok = true;
       if (j % kMetaBatch == 0)
         ok = mbar_wait(smem_u32(&bars->meta_full[j / kMetaBatch % kMetaBatches]), (j / kMetaSlots) & 1, abort_flag);
-      if (!__all_sync(~0u, ok && mbar_wait(smem_u32(&bars->s_full[tile]), j & 1, abort_flag))) return false;
+      if (!__all_sync(~0u, ok && mbar_wait(smem_u32(&bars->s_full[tile][j & 1]), (j >> 1) & 1, abort_flag))) return false;
       tc_fence_after();
       const TileMeta& M = metas[j % kMetaSlots];
-      uint32_t r[2][32];
-      load_scores(r);
-      if (!BIAS) free_scores();
-      const int k0 = M.key0[0], k1 = M.key0[kTileCells - 1] + kKv8CellKeys - 1;
+      const uint32_t sb = s_tmem + kTileKeys * (j & 1);
       // whole: every key of the tile is seen by all of the warp's rows
-      const bool whole = __all_sync(~0u, M.there == (1 << kTileCells) - 1 && k1 - k0 == kTileKeys - 1 && row.lo <= k0 &&
-                                             k1 <= row.hi);
+      const bool whole = __all_sync(~0u, row.lo <= M.key0[0] && M.last <= row.hi);
+      const float4 ks = *reinterpret_cast<const float4*>(M.ks), lv = *reinterpret_cast<const float4*>(M.lv);
+      const float kk_[4] = {ks.x * scl2, ks.y * scl2, ks.z * scl2, ks.w * scl2}, lv_[4] = {lv.x, lv.y, lv.z, lv.w};
       // raw: without a bias z is one fused multiply-add of the raw score, done again in the second pass.  m then is not
       // the exact maximum of those sums, but within a rounding of it, so scores whose rounding is not small against 1 take
-      // the other path.
+      // the other path: z made cell by cell in tensor memory, by a loop, which keeps the hot path short (the roles' code
+      // together is what the instruction caches hold).
       bool raw = !BIAS && whole;
       float top = -INFINITY;
-      if (BIAS) {
-        float most = 0.f;
-        if (behind)
+      if (raw) {
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(sb + 32 * c, r);
+          tmem_ld_wait();
 #pragma unroll
-          for (int cell = 0; cell < kTileCells; ++cell)
-            scores_quick(M, cell, &r[cell / 2][16 * (cell % 2)], per_cap, most);
-        if (__all_sync(~0u, behind && most <= 0.36f)) {
-          if (!whole)
+          for (int e = 0; e < 2; ++e) {
+            float y = __uint_as_float(r[16 * e]);
 #pragma unroll
-            for (int cell = 0; cell < kTileCells; ++cell) {
-              const uint32_t bits = (M.there >> cell) & 1 ? cell_bits(row, seq.prefix, M.key0[cell]) : 0u;
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                if (!((bits >> i) & 1u)) r[cell / 2][16 * (cell % 2) + i] = 0xff800000u;
-            }
-#pragma unroll
-          for (int i = 0; i < 64; i += 2)
-            top = fmaxf(fmaxf(top, __uint_as_float(r[i / 32][i % 32])), __uint_as_float(r[i / 32][i % 32 + 1]));
-        } else {
-          load_scores(r);
-#pragma unroll
-          for (int cell = 0; cell < kTileCells; ++cell)
-            top = fmaxf(top, scores(M, cell, &r[cell / 2][16 * (cell % 2)], two_over_cap));
-        }
-        free_scores();
-      } else {
-        if (raw) {
-#pragma unroll
-          for (int cell = 0; cell < kTileCells; ++cell) {
-            const uint32_t* x = &r[cell / 2][16 * (cell % 2)];
-            float y = __uint_as_float(x[0]);
-#pragma unroll
-            for (int i = 1; i < 15; i += 2) y = fmaxf(fmaxf(y, __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
-            y = fmaxf(y, __uint_as_float(x[15]));
-            top = fmaxf(top, fmaf(y, M.ks[cell] * scl * kLog2e, M.lv[cell]));
+            for (int i = 1; i < 15; i += 2) y = fmaxf(fmaxf(y, __uint_as_float(r[16 * e + i])), __uint_as_float(r[16 * e + i + 1]));
+            y = fmaxf(y, __uint_as_float(r[16 * e + 15]));
+            top = fmaxf(top, fmaf(y, c ? kk_[2 + e] : kk_[e], c ? lv_[2 + e] : lv_[e]));
           }
-          raw = __all_sync(~0u, fabsf(top) < 65536.0f);
         }
-        if (!raw) {
-          top = -INFINITY;
-#pragma unroll
-          for (int cell = 0; cell < kTileCells; ++cell)
-            top = fmaxf(top, scores(M, cell, &r[cell / 2][16 * (cell % 2)], two_over_cap));
-        }
+        raw = __all_sync(~0u, fabsf(top) < 65536.0f);
+      }
+      if (!raw) {
+        top = transform(M, sb, whole, behind, two_over_cap, per_cap);
       }
       const bool rise = top > m + kTileSlack, any = __any_sync(~0u, rise);
       if (any) {
@@ -361,35 +354,38 @@ struct TileSoftmax {
           }
         }
       }
-      uint32_t p[2][16];
+      const float4 iv = *reinterpret_cast<const float4*>(M.iv);
+#pragma unroll 1
+      for (int c = 0; c < 2; ++c) {
+        uint32_t r[32], p[16];
+        tmem_ld_32x32b_x32(sb + 32 * c, r);
+        tmem_ld_wait();
 #pragma unroll
-      for (int cell = 0; cell < kTileCells; ++cell) {
-        const float kk = raw ? M.ks[cell] * scl * kLog2e : 1.0f, add = raw ? M.lv[cell] - m : -m;
-        const uint64_t kk2 = pack2(kk, kk), add_2 = pack2(add, add);
-        uint64_t sum2 = 0;
-        float x, y;
+        for (int e = 0; e < 2; ++e) {
+          const float kk = raw ? (c ? kk_[2 + e] : kk_[e]) : 1.0f, add = raw ? (c ? lv_[2 + e] : lv_[e]) - m : -m;
+          const uint64_t kk2 = pack2(kk, kk), add_2 = pack2(add, add);
+          uint64_t sum2 = 0;
+          float x, y;
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-          const uint32_t* q = &r[cell / 2][16 * (cell % 2) + i];
-          unpack2(fma2(pack2(__uint_as_float(q[0]), __uint_as_float(q[1])), kk2, add_2), x, y);
-          x = fast_exp2(x), y = fast_exp2(y);
-          sum2 = add2(sum2, pack2(x, y));
-          p[cell / 2][8 * (cell % 2) + i / 2] = pack_f16(x, y);
+          for (int i = 0; i < 16; i += 2) {
+            const uint32_t* q = &r[16 * e + i];
+            unpack2(fma2(pack2(__uint_as_float(q[0]), __uint_as_float(q[1])), kk2, add_2), x, y);
+            x = fast_exp2(x), y = fast_exp2(y);
+            sum2 = add2(sum2, pack2(x, y));
+            p[8 * e + i / 2] = pack_f16(x, y);
+          }
+          unpack2(sum2, x, y);
+          x += y;
+          const float w = c ? (e ? iv.w : iv.z) : (e ? iv.y : iv.x);
+          if (x != 0.f) l = fmaf(x, w, l);  // a cell out of sight adds nothing, even where its scale is NaN
         }
-        unpack2(sum2, x, y);
-        x += y;
-        if (x != 0.f) l = fmaf(x, M.iv[cell], l);  // a cell out of sight adds nothing, even where its scale is NaN
+        tmem_st_32x32b_x16(sb + 16 * c, p);  // over scores that this thread has read
       }
-      // the MMAs have read the last key tile's P
-      if (j > 0 && !__all_sync(~0u, mbar_wait(smem_u32(&bars->pv_done[tile]), (j - 1) & 1, abort_flag))) return false;
-      tc_fence_after();
-      tmem_st_32x32b_x16(p_tmem, p[0]);
-      tmem_st_32x32b_x16(p_tmem + 16, p[1]);
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane_id() == 0) {
-        mbar_arrive_remote(p_full);
+        mbar_arrive_remote(p_full + 8 * (j & 1));
         if (j % kMetaBatch == kMetaBatch - 1)
           mbar_arrive(smem_u32(&bars->meta_empty[j / kMetaBatch % kMetaBatches]));
       }
@@ -507,52 +503,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     const uint32_t q_lo = desc_lo(sb + L::q), k_lo = desc_lo(sb + L::k), v_lo = desc_lo(sb + L::v);
     constexpr uint32_t kKFull = offsetof(TileBars, k_full), kVFull = offsetof(TileBars, v_full),
                        kKEmpty = offsetof(TileBars, k_empty), kVEmpty = offsetof(TileBars, v_empty),
-                       kSFree = offsetof(TileBars, s_free), kPFull = offsetof(TileBars, p_full),
+                       kPFull = offsetof(TileBars, p_full),
                        kSFull = offsetof(TileBars, s_full), kPvDone = offsetof(TileBars, pv_done),
                        kDrain = offsetof(TileBars, drain);
     auto wait_pair = [&](uint32_t b, uint32_t par) { return __all_sync(~0u, mbar_wait_cluster(b, par, &abort_flag)) != 0; };
     auto wait = [&](uint32_t b, uint32_t par) { return __all_sync(~0u, mbar_wait(b, par, &abort_flag)) != 0; };
-    auto scores = [&](int t, int st) {
+    auto scores = [&](int t, int st, uint32_t buf) {
       const uint32_t qa = q_lo + t * (L::kQ / 16), ka = k_lo + st * (L::kHalf / 16);
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
-        umma_f16_ss_pair<kHiK, kHiK, kIdS>(tm + kTileKeys * t, qa + ((i / 4) * (128 * 128) + (i % 4) * 32) / 16,
+        umma_f16_ss_pair<kHiK, kHiK, kIdS>(tm + 2 * kTileKeys * t + kTileKeys * buf, qa + ((i / 4) * (128 * 128) + (i % 4) * 32) / 16,
                                            ka + ((i / 4) * (32 * 128) + (i % 4) * 32) / 16, i > 0, on);
-      umma_commit_both(bar + kSFull + 8 * t, on);
+      umma_commit_both(bar + kSFull + 8 * (2 * t + buf), on);
     };
     bool ok = wait_pair(bar + kKFull, 0);
     if (ok) {
       tc_fence_after();
-      scores(0, 0);
-      if (num_t > 1) scores(1, 0);
+      scores(0, 0, 0);
+      if (num_t > 1) scores(1, 0, 0);
       umma_commit_both(bar + kKEmpty, on);
     }
     int st = 0, nx = 1 % kTileStages;     // stage of key tile j and of j + 1
     uint32_t st_par = 0, nx_par = 0, par = 0;
-    // what s_free and p_full hand over lies in tensor memory, ordered by the tcgen05 fences around the barriers
     for (int j = 0; ok && j < num; ++j) {
       if (j + 1 < num) {
-        ok = wait_pair(bar + kKFull + 8 * nx, nx_par);
+        if (!(ok = wait_pair(bar + kKFull + 8 * nx, nx_par))) break;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (!ok || t >= num_t) break;
-          if (!(ok = wait(bar + kSFree + 8 * t, par))) break;
+          // S goes over the P that the MMAs of key tile j - 1 read: MMAs of different shapes keep no order by themselves
+          if (j > 0 && !(ok = wait(bar + kPvDone + 8 * t, par ^ 1))) break;
           tc_fence_after();
-          scores(t, nx);
+          scores(t, nx, par ^ 1);
         }
         if (!ok) break;
         umma_commit_both(bar + kKEmpty + 8 * nx, on);
       }
+      // what p_full hands over lies in tensor memory, ordered by the tcgen05 fences around the barrier
       ok = wait_pair(bar + kVFull + 8 * st, st_par);
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         if (!ok || t >= num_t) break;
-        if (!(ok = wait(bar + kPFull + 8 * t, par))) break;
+        if (!(ok = wait(bar + kPFull + 8 * (2 * t + par), (j >> 1) & 1))) break;
         tc_fence_after();
         const uint32_t va = v_lo + st * (L::kHalf / 16);
 #pragma unroll
         for (int i = 0; i < kTileKeys / 16; ++i)
-          umma_f16_ts_pair<kHiV, kIdO>(tm + 256 + D * t, tm + 128 + 32 * t + 8 * i, va + i * D, i > 0 ? 1 : j, on);
+          umma_f16_ts_pair<kHiV, kIdO>(tm + 256 + D * t, tm + 2 * kTileKeys * t + kTileKeys * par + 8 * i, va + i * D, i > 0 ? 1 : j, on);
         umma_commit_both(bar + kPvDone + 8 * t, on);
       }
       if (ok) umma_commit_both(bar + kVEmpty + 8 * st, on);
@@ -588,7 +585,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
       const int c = lane % kTileCells;
       const float vs = sc.y < kLeastScale ? kLeastScale : sc.y;  // NaN stays
       M.at[c] = at, M.key0[c] = key0, M.ks[c] = sc.x, M.lv[c] = __log2f(vs), M.iv[c] = __frcp_rn(vs);
-      if (c == 0) M.there = (there >> (lane & ~(kTileCells - 1))) & ((1 << kTileCells) - 1);
+      const int next = __shfl_down_sync(~0u, key0, kTileCells - 1);  // of a tile's first lane: its last cell's first key
+      if (c == 0) {
+        const int mapped = (there >> (lane & ~(kTileCells - 1))) & ((1 << kTileCells) - 1);
+        M.there = mapped;
+        M.last = mapped == (1 << kTileCells) - 1 && next - key0 == kTileKeys - kKv8CellKeys ? key0 + kTileKeys - 1 : INT_MAX;
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&bars.meta_full[b % kMetaBatches]));
     }
@@ -644,13 +646,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
       const uint32_t lanes = static_cast<uint32_t>(warp % 4) << 21;  // (32 * quarter) << 16
       const int r = tile * 128 + (warp % 4) * 32 + lane, rr = min(global_row(r), r1 - 1);
       const bool mine = global_row(r) < r1;
-      TileSoftmax<D, BIAS> sm{a, seq, metas, &bars, &abort_flag, (tmem + 64 * tile) | lanes,
-                              (tmem + 128 + 32 * tile) | lanes, (tmem + 256 + D * tile) | lanes,
-                              mapa_shared(smem_u32(&bars.s_free[tile]), 0), mapa_shared(smem_u32(&bars.p_full[tile]), 0), tile,
+      TileSoftmax<D, BIAS> sm{a, seq, metas, &bars, &abort_flag, (tmem + 2 * kTileKeys * tile) | lanes,
+                              (tmem + 256 + D * tile) | lanes, mapa_shared(smem_u32(&bars.p_full[tile][0]), 0), tile,
                               kv8_row(a, seq, rr / a.group), mine ? qscale[r] : 0.f,
                               a.slopes ? a.slopes[h * a.group + rr % a.group] * kLog2e : 0.f, kNoMax, 0.f};
       bool ok = sm.run(n);
-      if (ok && n > 0) ok = __all_sync(~0u, mbar_wait(smem_u32(&bars.pv_done[tile]), (n - 1) & 1, &abort_flag));
+      // the last two phases, one by one: the one before the last may still be open, and looks like the last but two
+      for (int j = max(n - 2, 0); j < n && ok; ++j)
+        ok = __all_sync(~0u, mbar_wait(smem_u32(&bars.pv_done[tile]), j & 1, &abort_flag));
       tc_fence_after();
       const float sum = ok ? sm.l : NAN;
       const float inv = a.nsplit > 1 ? 1.0f : (sum == 0.f ? 0.f : 1.0f / sum);
