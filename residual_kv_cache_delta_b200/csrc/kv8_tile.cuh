@@ -7,18 +7,19 @@
 // of K, half of V's dimensions.  With one CTA per tile the shared memory that feeds S (M = N = 128, both operands from
 // there) is the limit: 117 clocks per 128 x 128 x 16 MMA measured against 64 for the pair's 256 x 128 x 16, and every
 // code is converted twice.  Roles in each CTA:
-//   warps 0-3, 4-7  softmax of row tile 0 and 1: a thread owns a row (a tensor-memory lane)
-//   warps 8-9, 10-11  load codes of K, of V into registers, two key tiles ahead, and turn them into fp16 operands in shared
-//                   memory; K and V, which lie alike (rows of keys), are a K-major and an MN-major operand
-//   warp 12         issues the MMAs (first CTA);  warp 13 looks up block ids and scales, eight key tiles at a time
-//   warps 14, 15    of the second CTA pass on that its K or V is in place: a release at cluster scope takes about 1000
+//   warps 0-15      softmax: warp w takes tensor-memory lanes 32 (w % 4) .. of row tile (w / 4) % 2 and half w / 8 of a key
+//                   tile's columns; a thread owns half of a row and agrees with its partner on the row's maximum
+//   warps 16-17, 18-19  load codes of K, of V into registers, two key tiles ahead, and turn them into fp16 operands in
+//                   shared memory; K and V, which lie alike (rows of keys), are a K-major and an MN-major operand
+//   warp 20         issues the MMAs (first CTA);  warp 21 looks up block ids and scales, eight key tiles at a time
+//   warps 22, 23    of the second CTA pass on that its K or V is in place: a release at cluster scope takes about 1000
 //                   clocks, too long for the converters
 // Tiles of 64 keys leave tensor memory for two S buffers per row tile beside O: a tile's S is made while the softmax of the
 // one before it runs, and P is written over the columns of S that it came from, so that the softmax warps, whose exp2 (16 a
 // clock and SM) takes as long as the MMAs, do not wait for S.  (128-key tiles with one S buffer: the chain S, softmax, P V
-// of a row tile took 5400 clocks per 128 keys, of which the MMAs need 2048.)  The softmax goes through a tile's scores twice
-// in tensor memory, 32 at a time by loops: held in registers with unrolled code, the warps' different programs evicted
-// each other from the instruction caches.
+// of a row tile took 5400 clocks per 128 keys, of which the MMAs need 2048.)  A row's scores are read twice from tensor
+// memory, and what few tiles need is a loop: with all of them in registers and unrolled code, the warps' different programs
+// evicted each other from the instruction caches.
 //
 // Codes are exact in fp16; scales stay out of the operands as in kv8_stream.cuh: the K scale multiplies the fp32 score,
 // the V scale is part of the exponent z = score + log2(v scale), and the sum of weights takes it out again.  The running
@@ -33,7 +34,7 @@
 
 namespace dkv {
 
-constexpr int kTileThreads = 512, kTileRows = 512, kTileKeys = 64, kTileCells = kTileKeys / kKv8CellKeys;
+constexpr int kTileThreads = 768, kTileRows = 512, kTileKeys = 64, kTileCells = kTileKeys / kKv8CellKeys;
 constexpr int kTileStages = 4;       // of K and of V
 constexpr int kTileAhead = 2;        // key tiles in a converter's registers
 constexpr float kTileSlack = 8.0f;   // log2 of the most a weight may exceed 1 before the maximum is raised (fp16: 2^16)
@@ -60,7 +61,7 @@ struct TileBars {
   // per row tile and S buffer, since S and the softmax may be two key tiles ahead of who waits for them:
   uint64_t p_full[2][2];                             // of the pair, in the first CTA: both CTAs' softmax warps arrive
   uint64_t k_full[kTileStages], v_full[kTileStages];    // of each CTA's converters; in the first, the second's word too
-  uint64_t k_empty[kTileStages], v_empty[kTileStages], pv_done[2], drain;  // in both: the MMAs' commits arrive
+  uint64_t k_empty[kTileStages], v_empty[kTileStages], pv_done[2], o_full[2], drain;  // in both: the MMAs' commits arrive
   uint64_t s_full[2][2];                             // in both
 };
 constexpr int kTileBars = sizeof(TileBars) / 8;
@@ -202,7 +203,7 @@ struct TileCodes {
   }
 };
 
-// Softmax of a CTA's 128 rows of one row tile by four warps.  BIAS: scores may be capped or biased.
+// Softmax of a CTA's 128 rows of one row tile by eight warps, a thread half a row.  BIAS: scores may be capped or biased.
 template <int D, bool BIAS>
 struct TileSoftmax {
   const Kv8Attn& a;
@@ -212,7 +213,8 @@ struct TileSoftmax {
   volatile int* abort_flag;
   uint32_t s_tmem, o_tmem;  // of this warp's lanes: the first S buffer, O
   uint32_t p_full;          // cluster address of the pair's barrier of the first S buffer
-  int tile;
+  float* tops;              // the row's maxima of this half; the other half's are 256 floats on or back
+  int tile, half, meet;     // meet: barrier of the two warps of the same rows
   Kv8Row row;
   float scl, slope;  // row scale times the softmax scale (natural units); slope in log2 units
   float m, l;
@@ -259,11 +261,11 @@ struct TileSoftmax {
     }
   }
 
-  // The tile's scores in tensor memory as z, masked unless `whole`; returns the row's maximum.
+  // The thread's scores in tensor memory as z, masked unless `whole`; returns their maximum.
   __device__ __forceinline__ float transform(const TileMeta& M, uint32_t s_tmem, bool whole, bool behind, float two_over_cap, float per_cap) {
     float top = -INFINITY;
 #pragma unroll 1
-    for (int cell = 0; cell < kTileCells; ++cell) {
+    for (int cell = 2 * half; cell < 2 * half + 2; ++cell) {
       uint32_t r[16];
       tmem_ld_32x32b_x16(s_tmem + 16 * cell, r);
       tmem_ld_wait();
@@ -297,54 +299,60 @@ struct TileSoftmax {
     const float per_cap = BIAS && a.softcap > 0.f ? 1.0f / a.softcap : 0.f;
     const float scl2 = scl * kLog2e;
     const bool behind = BIAS && __all_sync(~0u, slope == 0.f || seq.prefix <= row.pos + 1);
+    bool ok = true;  // no wait of this warp has run out; both warps of a row leave together, at the barrier where they meet
     for (int j = 0; j < n; ++j) {
-      bool ok = true;
       if (j % kMetaBatch == 0)
-        ok = mbar_wait(smem_u32(&bars->meta_full[j / kMetaBatch % kMetaBatches]), (j / kMetaSlots) & 1, abort_flag);
-      if (!__all_sync(~0u, ok && mbar_wait(smem_u32(&bars->s_full[tile][j & 1]), (j >> 1) & 1, abort_flag))) return false;
+        ok = ok && mbar_wait(smem_u32(&bars->meta_full[j / kMetaBatch % kMetaBatches]), (j / kMetaSlots) & 1, abort_flag);
+      ok = __all_sync(~0u, ok && mbar_wait(smem_u32(&bars->s_full[tile][j & 1]), (j >> 1) & 1, abort_flag));
       tc_fence_after();
       const TileMeta& M = metas[j % kMetaSlots];
       const uint32_t sb = s_tmem + kTileKeys * (j & 1);
       // whole: every key of the tile is seen by all of the warp's rows
       const bool whole = __all_sync(~0u, row.lo <= M.key0[0] && M.last <= row.hi);
-      const float4 ks = *reinterpret_cast<const float4*>(M.ks), lv = *reinterpret_cast<const float4*>(M.lv);
-      const float kk_[4] = {ks.x * scl2, ks.y * scl2, ks.z * scl2, ks.w * scl2}, lv_[4] = {lv.x, lv.y, lv.z, lv.w};
+      const float2 ks = reinterpret_cast<const float2*>(M.ks)[half], lv = reinterpret_cast<const float2*>(M.lv)[half];
+      const float kk[2] = {ks.x * scl2, ks.y * scl2};
+      uint32_t r[32];
       // raw: without a bias z is one fused multiply-add of the raw score, done again in the second pass.  m then is not
       // the exact maximum of those sums, but within a rounding of it, so scores whose rounding is not small against 1 take
-      // the other path: z made cell by cell in tensor memory, by a loop, which keeps the hot path short (the roles' code
-      // together is what the instruction caches hold).
+      // the other path: z made cell by cell in tensor memory.
       bool raw = !BIAS && whole;
       float top = -INFINITY;
       if (raw) {
-#pragma unroll 1
-        for (int c = 0; c < 2; ++c) {
-          uint32_t r[32];
-          tmem_ld_32x32b_x32(sb + 32 * c, r);
-          tmem_ld_wait();
+        tmem_ld_32x32b_x32(sb + 32 * half, r);
+        tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            float y = __uint_as_float(r[16 * e]);
+        for (int e = 0; e < 2; ++e) {
+          float y[4];
 #pragma unroll
-            for (int i = 1; i < 15; i += 2) y = fmaxf(fmaxf(y, __uint_as_float(r[16 * e + i])), __uint_as_float(r[16 * e + i + 1]));
-            y = fmaxf(y, __uint_as_float(r[16 * e + 15]));
-            top = fmaxf(top, fmaf(y, c ? kk_[2 + e] : kk_[e], c ? lv_[2 + e] : lv_[e]));
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t* x = &r[16 * e + 4 * i];
+            y[i] = fmaxf(fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])), fmaxf(__uint_as_float(x[2]), __uint_as_float(x[3])));
           }
+          top = fmaxf(top, fmaf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), kk[e], e ? lv.y : lv.x));
         }
         raw = __all_sync(~0u, fabsf(top) < 65536.0f);
       }
       if (!raw) {
         top = transform(M, sb, whole, behind, two_over_cap, per_cap);
+        tmem_ld_32x32b_x32(sb + 32 * half, r);
+        tmem_ld_wait();
       }
+      // the row's maximum of both halves; both warps have read their scores
+      tops[512 * (j & 1)] = top;
+      tc_fence_before();
+      if (named_bar_or(meet, 64, !ok)) return false;
+      tc_fence_after();
+      top = fmaxf(top, tops[512 * (j & 1) + (half ? -256 : 256)]);
       const bool rise = top > m + kTileSlack, any = __any_sync(~0u, rise);
       if (any) {
         const float now = rise ? top : m, fix = fast_exp2(m - now);
         m = now;
         l *= fix;
         if (j > 0) {
-          if (!__all_sync(~0u, mbar_wait(smem_u32(&bars->pv_done[tile]), (j - 1) & 1, abort_flag))) return false;
+          ok = __all_sync(~0u, mbar_wait(smem_u32(&bars->pv_done[tile]), (j - 1) & 1, abort_flag));
           tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < D / 16; ++c) {
+          for (int c = half * (D / 32); c < (half + 1) * (D / 32); ++c) {
             uint32_t x[16];
             tmem_ld_32x32b_x16(o_tmem + 16 * c, x);
             tmem_ld_wait();
@@ -354,33 +362,27 @@ struct TileSoftmax {
           }
         }
       }
-      const float4 iv = *reinterpret_cast<const float4*>(M.iv);
-#pragma unroll 1
-      for (int c = 0; c < 2; ++c) {
-        uint32_t r[32], p[16];
-        tmem_ld_32x32b_x32(sb + 32 * c, r);
-        tmem_ld_wait();
+      const float2 iv = reinterpret_cast<const float2*>(M.iv)[half];
+      uint32_t p[16];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float kk = raw ? (c ? kk_[2 + e] : kk_[e]) : 1.0f, add = raw ? (c ? lv_[2 + e] : lv_[e]) - m : -m;
-          const uint64_t kk2 = pack2(kk, kk), add_2 = pack2(add, add);
-          uint64_t sum2 = 0;
-          float x, y;
+      for (int e = 0; e < 2; ++e) {
+        const float mul = raw ? kk[e] : 1.0f, add = raw ? (e ? lv.y : lv.x) - m : -m;
+        const uint64_t mul_2 = pack2(mul, mul), add_2 = pack2(add, add);
+        uint64_t sum2 = 0;
+        float x, y;
 #pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            const uint32_t* q = &r[16 * e + i];
-            unpack2(fma2(pack2(__uint_as_float(q[0]), __uint_as_float(q[1])), kk2, add_2), x, y);
-            x = fast_exp2(x), y = fast_exp2(y);
-            sum2 = add2(sum2, pack2(x, y));
-            p[8 * e + i / 2] = pack_f16(x, y);
-          }
-          unpack2(sum2, x, y);
-          x += y;
-          const float w = c ? (e ? iv.w : iv.z) : (e ? iv.y : iv.x);
-          if (x != 0.f) l = fmaf(x, w, l);  // a cell out of sight adds nothing, even where its scale is NaN
+        for (int i = 0; i < 16; i += 2) {
+          const uint32_t* q = &r[16 * e + i];
+          unpack2(fma2(pack2(__uint_as_float(q[0]), __uint_as_float(q[1])), mul_2, add_2), x, y);
+          x = fast_exp2(x), y = fast_exp2(y);
+          sum2 = add2(sum2, pack2(x, y));
+          p[8 * e + i / 2] = pack_f16(x, y);
         }
-        tmem_st_32x32b_x16(sb + 16 * c, p);  // over scores that this thread has read
+        unpack2(sum2, x, y);
+        x += y;
+        if (x != 0.f) l = fmaf(x, e ? iv.y : iv.x, l);  // a cell out of sight adds nothing, even where its scale is NaN
       }
+      tmem_st_32x32b_x16(sb + 16 * half, p);  // over scores of the first half, which both warps have read
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
@@ -390,7 +392,7 @@ struct TileSoftmax {
           mbar_arrive(smem_u32(&bars->meta_empty[j / kMetaBatch % kMetaBatches]));
       }
     }
-    return true;
+    return ok;
   }
 };
 
@@ -402,6 +404,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
   __shared__ __align__(8) TileBars bars;
   __shared__ TileMeta metas[kMetaSlots];
   __shared__ float qscale[256];
+  __shared__ float tops[2 * 512];  // two key tiles in turn: maxima of 256 rows' first halves, of their second halves
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
   uint8_t* smem = align_shared<1024>(smem_raw);
@@ -430,10 +433,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     const uint32_t b = smem_u32(&bars);
     constexpr int kP = 2 * kMetaBatches, kFull = kP + 4, kRest = kFull + 2 * kTileStages;
     for (int i = 0; i < kTileBars; ++i)  // meta_empty: the CTA's warps that read a batch
-      mbar_init(b + 8 * i, i < kMetaBatches ? 1 : i < kP ? 4 * tiles + 4 : i < kFull ? 8 : i < kRest ? (rank == 0 ? 3 : 2) : 1);
+      mbar_init(b + 8 * i, i < kMetaBatches ? 1 : i < kP ? 8 * tiles + 4 : i < kFull ? 16 : i < kRest ? (rank == 0 ? 3 : 2) : 1);
     fence_barrier_init();
   }
-  if (warp == 12) {
+  if (warp == 20) {
     tmem_alloc_pair(smem_u32(&tmem_base), 512);
     tmem_relinquish_pair();
   }
@@ -504,7 +507,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     constexpr uint32_t kKFull = offsetof(TileBars, k_full), kVFull = offsetof(TileBars, v_full),
                        kKEmpty = offsetof(TileBars, k_empty), kVEmpty = offsetof(TileBars, v_empty),
                        kPFull = offsetof(TileBars, p_full),
-                       kSFull = offsetof(TileBars, s_full), kPvDone = offsetof(TileBars, pv_done),
+                       kSFull = offsetof(TileBars, s_full), kPvDone = offsetof(TileBars, pv_done), kOFull = offsetof(TileBars, o_full),
                        kDrain = offsetof(TileBars, drain);
     auto wait_pair = [&](uint32_t b, uint32_t par) { return __all_sync(~0u, mbar_wait_cluster(b, par, &abort_flag)) != 0; };
     auto wait = [&](uint32_t b, uint32_t par) { return __all_sync(~0u, mbar_wait(b, par, &abort_flag)) != 0; };
@@ -550,7 +553,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
 #pragma unroll
         for (int i = 0; i < kTileKeys / 16; ++i)
           umma_f16_ts_pair<kHiV, kIdO>(tm + 256 + D * t, tm + 2 * kTileKeys * t + kTileKeys * par + 8 * i, va + i * D, i > 0 ? 1 : j, on);
-        umma_commit_both(bar + kPvDone + 8 * t, on);
+        umma_commit_both(bar + (j + 1 < num ? kPvDone : kOFull) + 8 * t, on);
       }
       if (ok) umma_commit_both(bar + kVEmpty + 8 * st, on);
       par ^= 1;
@@ -638,29 +641,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     }
   };
 
-  // per sub-partition: 2 x 160 + 136 + 56 = 4 x 128 registers a thread, what the CTA was launched with
-  if (warp < 8) {
-    regs_take<160>();
-    const int tile = warp / 4;
+  // per sub-partition: 4 x 80 + 104 + 56 = 6 x 80 registers a thread, what the CTA was launched with
+  if (warp < 16) {
+    const int tile = (warp / 4) & 1, half = warp / 8;
     if (tile < tiles) {
       const uint32_t lanes = static_cast<uint32_t>(warp % 4) << 21;  // (32 * quarter) << 16
       const int r = tile * 128 + (warp % 4) * 32 + lane, rr = min(global_row(r), r1 - 1);
       const bool mine = global_row(r) < r1;
       TileSoftmax<D, BIAS> sm{a, seq, metas, &bars, &abort_flag, (tmem + 2 * kTileKeys * tile) | lanes,
-                              (tmem + 256 + D * tile) | lanes, mapa_shared(smem_u32(&bars.p_full[tile][0]), 0), tile,
+                              (tmem + 256 + D * tile) | lanes, mapa_shared(smem_u32(&bars.p_full[tile][0]), 0),
+                              tops + 256 * half + r, tile, half, 1 + warp % 8,
                               kv8_row(a, seq, rr / a.group), mine ? qscale[r] : 0.f,
                               a.slopes ? a.slopes[h * a.group + rr % a.group] * kLog2e : 0.f, kNoMax, 0.f};
       bool ok = sm.run(n);
-      // the last two phases, one by one: the one before the last may still be open, and looks like the last but two
-      for (int j = max(n - 2, 0); j < n && ok; ++j)
-        ok = __all_sync(~0u, mbar_wait(smem_u32(&bars.pv_done[tile]), j & 1, &abort_flag));
+      // not pv_done, of which up to two phases may be open or done here
+      if (ok && n > 0) ok = __all_sync(~0u, mbar_wait(smem_u32(&bars.o_full[tile]), 0, &abort_flag));
       tc_fence_after();
-      const float sum = ok ? sm.l : NAN;
+      // the row's sum of both halves
+      named_bar_sync(1 + warp % 8, 64);
+      sm.tops[0] = sm.l;
+      named_bar_sync(1 + warp % 8, 64);
+      const float sum = ok ? sm.l + sm.tops[half ? -256 : 256] : NAN;
       const float inv = a.nsplit > 1 ? 1.0f : (sum == 0.f ? 0.f : 1.0f / sum);
       const int64_t at = static_cast<int64_t>(seq.q0 + rr / a.group) * hq + h * a.group + rr % a.group;
       const int64_t prow = split * (a.total_q * hq) + at;
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = half * (D / 64); c < (half + 1) * (D / 64); ++c) {
         uint32_t x[32];
         if (n > 0) {
           tmem_ld_32x32b_x32(sm.o_tmem + 32 * c, x);
@@ -692,26 +698,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
           }
         }
       }
-      if (mine) {
+      if (mine && half == 0) {
         if (a.nsplit > 1) a.ml[prow] = make_float2(sm.m, sum);
         else if (a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (sm.m + log2f(sum)) * kLn2;
       }
       tc_fence_before();
     }
-  } else if (warp < 12) {
-    regs_take<136>();
-    if (warp < 10) convert(std::false_type(), L::k, bars.k_full, bars.k_empty, warp - 8);
-    else convert(std::true_type(), L::v, bars.v_full, bars.v_empty, warp - 10);
+  } else if (warp < 20) {
+    regs_take<104>();
+    if (warp < 18) convert(std::false_type(), L::k, bars.k_full, bars.k_empty, warp - 16);
+    else convert(std::true_type(), L::v, bars.v_full, bars.v_empty, warp - 18);
   } else {
     regs_give<56>();
-    if (warp == 12 && rank == 0 && n > 0) issue_mmas();
-    if (warp >= 14 && lane == 0 && rank == 1) pass_on(warp == 14 ? bars.k_full : bars.v_full);
+    if (warp == 20 && rank == 0 && n > 0) issue_mmas();
+    if (warp >= 22 && lane == 0 && rank == 1) pass_on(warp == 22 ? bars.k_full : bars.v_full);
     __syncwarp();
-    if (warp == 13) look_up();
+    if (warp == 21) look_up();
   }
   __syncthreads();
   cluster_sync_all();  // neither CTA leaves while the other's MMAs, commits or arrivals may reach it
-  if (warp == 12) {
+  if (warp == 20) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
   }
