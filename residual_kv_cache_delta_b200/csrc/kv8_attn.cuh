@@ -20,7 +20,7 @@ static Kv8Plan kv8_plan(const dkv_kv8_shape& sh, int num_seqs, int max_q, int sp
   Kv8Plan p;
   const bool tiles = sh.dtype != DKV_F32 && rows > kStreamMaxRows;
   p.tile = sh.dtype == DKV_F32 ? kSimpleRows : tiles ? kTileRows : rows <= 8 ? 8 : 16;
-  const int per_sm = sh.dtype == DKV_F32 ? 4 : p.tile == 8 ? 2 : 1;
+  const int per_sm = sh.dtype == DKV_F32 ? 4 : tiles ? 1 : sh.head_dim == 64 ? stream_ctas<64>(p.tile / 8) : stream_ctas<128>(p.tile / 8);
   const int64_t base = ceil_div64(rows, p.tile) * sh.num_kv_heads * std::max(num_seqs, 1);
   const int64_t cells = ceil_div64(span, kKv8CellKeys);
   const int64_t sms = tiles ? num_sms() / 2 : num_sms();  // the tcgen05 kernel's CTAs come in pairs
@@ -32,7 +32,9 @@ static Kv8Plan kv8_plan(const dkv_kv8_shape& sh, int num_seqs, int max_q, int sp
   double best = 0;
   for (int n = 1; n <= most; ++n) {
     const int64_t ctas = base * n;
-    double t = static_cast<double>(ceil_div64(ctas, sms)) * (static_cast<double>(cells) / n) +
+    // (a CTA alone on its SM waits for its own latencies and is hardly faster than two that share one)
+    double t = static_cast<double>(std::max<int64_t>(ceil_div64(ctas, sms), std::min(per_sm, 2))) *
+                   (static_cast<double>(cells) / n) +
                24.0 * static_cast<double>(ceil_div64(ctas, sms * per_sm));
     if (n > 1) t += 20.0 + (tiles ? 40.0 * static_cast<double>(ceil_div64(ctas, sms)) : 0.0);
     if (n == 1 || t < best) best = t, p.nsplit = n;

@@ -31,8 +31,12 @@ constexpr int kStreamWarps = 8;
 constexpr float kLeastScale = 8.271806125530277e-25f;  // 2^-80, below any scale that an append writes
 constexpr float kMaxSlack = 4.0f;  // log2 of the most a weight may exceed 1 before the maximum is raised
 
+// CTAs of an SM: two, unless 16 rows of 128 dimensions take the registers of both.  (64 dimensions, 16 rows: one CTA with
+// twice the stages left the warps' latencies in sight, 24.8 us for 8 sequences of 5 tokens.)
 template <int D>
-__host__ __device__ constexpr int stream_stages(int nt) { return (D == 128 ? 3 : 6) * (nt > 1 ? 2 : 1); }
+__host__ __device__ constexpr int stream_ctas(int nt) { return D == 128 && nt > 1 ? 1 : 2; }
+template <int D>
+__host__ __device__ constexpr int stream_stages(int nt) { return (D == 128 ? 6 : 12) / stream_ctas<D>(nt); }
 template <int D>
 constexpr size_t stream_smem(int nt) {
   return 1024 + static_cast<size_t>(kStreamWarps) * stream_stages<D>(nt) * 32 * D;
@@ -94,7 +98,7 @@ __device__ __forceinline__ void q_pairs(const uint4& w, float f, uint32_t* out) 
 
 // BIAS: scores may be capped or biased by distance.
 template <int D, bool E4M3, int NT, bool BIAS>
-__global__ void __launch_bounds__(kStreamWarps * 32, NT == 1 ? 2 : 1)
+__global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas<D>(NT))
     kv8_stream_kernel(const __grid_constant__ CUtensorMap map, const Kv8Attn a, int row_tiles) {
   constexpr int kSteps = D / 16, kStg = stream_stages<D>(NT), kRows = 8 * NT;
   constexpr uint32_t kCellBytes = 32 * D;

@@ -11,8 +11,8 @@ import ctypes
 import math
 import os
 from dataclasses import dataclass
-from functools import cached_property
-from typing import Optional
+from functools import lru_cache
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -396,8 +396,7 @@ def deltakv_decode_attention_topk(shape: Shape, k: int, mu: torch.Tensor, basis:
     _check(st, "deltakv_decode_attention_topk")
 
 
-@dataclass(frozen=True)
-class KV8Shape:
+class KV8Shape(NamedTuple):
     """Head geometry of one layer of the 8-bit cache (mirrors ``dkv_kv8_shape``); code "int8" or "e4m3"."""
 
     num_q_heads: int
@@ -407,16 +406,22 @@ class KV8Shape:
     dtype: torch.dtype = torch.bfloat16
     code: str = "int8"
 
-    @cached_property
+    @property
     def c(self) -> DkvKv8Shape:
         if self.dtype not in (torch.bfloat16, torch.float32) or self.code not in KV8_CODES:
             raise ValueError(f"KV8Shape: dtype {self.dtype}, code {self.code!r}")
         return DkvKv8Shape(self.num_q_heads, self.num_kv_heads, self.head_dim, self.block_tokens,
                            DKV_F32 if self.dtype == torch.float32 else DKV_BF16, KV8_CODES[self.code])
 
-    @cached_property
+    @property
     def code_dtype(self) -> torch.dtype:
         return torch.int8 if self.code == "int8" else torch.float8_e4m3fn
+
+
+@lru_cache(maxsize=64)
+def _kv8_shape(shape: KV8Shape):
+    """(pointer to the shape's structure, dtype of its codes): what every call needs of a shape."""
+    return ctypes.byref(shape.c), shape.code_dtype
 
 
 @dataclass
@@ -483,19 +488,25 @@ def _rows(t: torch.Tensor, n: int, heads: int, shape: KV8Shape, name: str, dev: 
     return t.data_ptr(), (st[0] if n > 1 else heads * d)
 
 
-def _kv8_cache(shape: KV8Shape, cache: KV8Cache, dev: int) -> DkvKv8Cache:
+def _kv8_cache(shape: KV8Shape, cache: KV8Cache, code: torch.dtype, dev: int):
     codes, H = cache.codes, shape.num_kv_heads
     nb = codes.shape[0]
-    return DkvKv8Cache(_sized(codes, (nb, H, 2, shape.block_tokens, shape.head_dim), shape.code_dtype, "cache.codes", dev),
-                       _sized(cache.scales, (nb, H, 2), torch.float32, "cache.scales", dev), nb)
+    return ctypes.byref(DkvKv8Cache(
+        _sized(codes, (nb, H, 2, shape.block_tokens, shape.head_dim), code, "cache.codes", dev),
+        _sized(cache.scales, (nb, H, 2), torch.float32, "cache.scales", dev), nb))
+
+
+# the current stream's handle, without a Stream object for each call where torch offers that
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
 def _call_on(dev: int, stream, fn, *args) -> int:
     """fn(*args, stream) with GPU ``dev`` current; its current stream unless one is given."""
     if torch.cuda.current_device() == dev:
-        return fn(*args, torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream))
+        return fn(*args, _raw_stream(dev) if stream is None else _stream(stream))
     with torch.cuda.device(dev):
-        return fn(*args, torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream))
+        return fn(*args, _raw_stream(dev) if stream is None else _stream(stream))
 
 
 def deltakv_kv8_append(shape: KV8Shape, cache: KV8Cache, k_new: torch.Tensor, v_new: torch.Tensor,
@@ -507,7 +518,8 @@ def deltakv_kv8_append(shape: KV8Shape, cache: KV8Cache, k_new: torch.Tensor, v_
     start_pos [num_seqs], block_tables [num_seqs, max_blocks] int32; rope [max_pos, rot_dim] fp32 (cosines, then
     sines); positions [total_new] int32 or None; q [total_new, H_q, d] with q_out of the same shape, or None."""
     dev, n = cache.codes.get_device(), k_new.shape[0]
-    cc = _kv8_cache(shape, cache, dev)
+    cs, code = _kv8_shape(shape)
+    cc = _kv8_cache(shape, cache, code, dev)
     num_seqs, max_blocks = block_tables.shape
     kp, ks = _rows(k_new, n, shape.num_kv_heads, shape, "k_new", dev)
     vp, vs = _rows(v_new, n, shape.num_kv_heads, shape, "v_new", dev)
@@ -524,7 +536,7 @@ def deltakv_kv8_append(shape: KV8Shape, cache: KV8Cache, k_new: torch.Tensor, v_
     if q is not None:
         qp, qs = _rows(q, n, shape.num_q_heads, shape, "q", dev)
         qo = _sized(q_out, (n, shape.num_q_heads, shape.head_dim), shape.dtype, "q_out", dev)
-    st = _call_on(dev, stream, load_library().deltakv_kv8_append, ctypes.byref(shape.c), ctypes.byref(cc), cr, kp, ks, vp,
+    st = _call_on(dev, stream, load_library().deltakv_kv8_append, cs, cc, cr, kp, ks, vp,
                   vs, _sized(cu_new, (num_seqs + 1,), torch.int32, "cu_new", dev),
                   _sized(start_pos, (num_seqs,), torch.int32, "start_pos", dev),
                   _sized(block_tables, (num_seqs, max_blocks), torch.int32, "block_tables", dev), max_blocks, num_seqs, n,
@@ -542,7 +554,8 @@ def deltakv_kv8_attention(shape: KV8Shape, cache: KV8Cache, q: torch.Tensor, cu_
     H_q] fp32 or None; cu_q [num_seqs+1] or None (one query token per sequence), context_lens [num_seqs], block_tables
     [num_seqs, max_blocks] int32; alibi_slopes [H_q] fp32, prefix_lens [num_seqs] and first_key [total_q] int32."""
     dev, n = cache.codes.get_device(), q.shape[0]
-    cc, i32, f32 = _kv8_cache(shape, cache, dev), torch.int32, torch.float32
+    cs, code = _kv8_shape(shape)
+    cc, i32, f32 = _kv8_cache(shape, cache, code, dev), torch.int32, torch.float32
     num_seqs, max_blocks = block_tables.shape
     H = shape.num_q_heads
     qp, qs = _rows(q, n, H, shape, "q", dev)
@@ -553,7 +566,7 @@ def deltakv_kv8_attention(shape: KV8Shape, cache: KV8Cache, q: torch.Tensor, cu_
             0 if prefix_lens is None else _sized(prefix_lens, (num_seqs,), i32, "prefix_lens", dev),
             0 if first_key is None else _sized(first_key, (n,), i32, "first_key", dev)))
     wsn = 0 if workspace is None else workspace.numel()
-    st = _call_on(dev, stream, load_library().deltakv_kv8_attention, ctypes.byref(shape.c), ctypes.byref(cc), score, qp,
+    st = _call_on(dev, stream, load_library().deltakv_kv8_attention, cs, cc, score, qp,
                   qs, 0 if cu_q is None else _sized(cu_q, (num_seqs + 1,), i32, "cu_q", dev),
                   _sized(context_lens, (num_seqs,), i32, "context_lens", dev),
                   _sized(block_tables, (num_seqs, max_blocks), i32, "block_tables", dev), max_blocks, num_seqs, n, max_q,
