@@ -1,25 +1,24 @@
 // Attention over the 8-bit cache for many query rows (prefill chunks, packed prompts) on tcgen05.
 //
 // A pair of CTAs takes up to 512 rows (a row is a query token and a head of the kv head's group) as two row tiles of 256,
-// 128 of each tile's rows per CTA, and a range of keys in tiles of 64 (four 16-key cells).  Per key tile and row tile
-//   S = Q K^T (M = 256 rows, N = 64 keys, K = d),   P = 2^(z - m),   O += P V (N = d, K = 64 keys)
-// as pair MMAs (cta_group::2) with S, P (fp16) and O in tensor memory.  Each CTA makes half of the shared operands: 32 keys
+// 128 of each tile's rows per CTA, and a range of keys in tiles of 128 (eight 16-key cells).  Per key tile and row tile
+//   S = Q K^T (M = 256 rows, N = 128 keys, K = d),   P = 2^(z - m),   O += P V (N = d, K = 128 keys)
+// as pair MMAs (cta_group::2) with S, P (fp16) and O in tensor memory.  Each CTA makes half of the shared operands: 64 keys
 // of K, half of V's dimensions.  With one CTA per tile the shared memory that feeds S (M = N = 128, both operands from
 // there) is the limit: 117 clocks per 128 x 128 x 16 MMA measured against 64 for the pair's 256 x 128 x 16, and every
 // code is converted twice.  Roles in each CTA:
-//   warps 0-15      softmax: warp w takes tensor-memory lanes 32 (w % 4) .. of row tile (w / 4) % 2 and half w / 8 of a key
-//                   tile's columns; a thread owns half of a row and agrees with its partner on the row's maximum
-//   warps 16-17, 18-19  load codes of K, of V into registers, two key tiles ahead, and turn them into fp16 operands in
-//                   shared memory; K and V, which lie alike (rows of keys), are a K-major and an MN-major operand
-//   warp 20         issues the MMAs (first CTA);  warp 21 looks up block ids and scales, eight key tiles at a time
-//   warps 22, 23    of the second CTA pass on that its K or V is in place: a release at cluster scope takes about 1000
+//   warps 0-3, 4-7  softmax of row tile 0 and 1: a thread owns a row (a tensor-memory lane)
+//   warps 8-11      load codes into registers, a key tile ahead, and turn them into fp16 operands in shared memory; K and V,
+//                   which lie alike (rows of keys), are a K-major and an MN-major operand
+//   warp 12         issues the MMAs (first CTA);  warp 13 looks up block ids and scales, four key tiles at a time
+//   warps 14, 15    of the second CTA pass on that its K or V is in place: a release at cluster scope takes about 1000
 //                   clocks, too long for the converters
-// Tiles of 64 keys leave tensor memory for two S buffers per row tile beside O: a tile's S is made while the softmax of the
-// one before it runs, and P is written over the columns of S that it came from, so that the softmax warps, whose exp2 (16 a
-// clock and SM) takes as long as the MMAs, do not wait for S.  (128-key tiles with one S buffer: the chain S, softmax, P V
-// of a row tile took 5400 clocks per 128 keys, of which the MMAs need 2048.)  A row's scores are read twice from tensor
-// memory, and what few tiles need is a loop: with all of them in registers and unrolled code, the warps' different programs
-// evicted each other from the instruction caches.
+// The softmax warps take registers from the others (184 against 96 and 48), so that a thread holds its row's 128 scores.  P is
+// written over the columns of S that it came from.  While one row tile is in its softmax the tensor cores work for the
+// other; the chain S, softmax, P V of a row tile, about 5000 clocks a key tile, is what a key tile takes (the MMAs need
+// 2048 of them, exp2 as many).  Measured on 2048 queries at 32768 keys, 1.16 ms here: two warps a row 1.24 ms; 64-key
+// tiles with two S buffers, so that S never waits, 1.32 ms with two warps a row and 1.36 to 1.42 ms with one (more
+// hand-overs for each key); the row tiles taking turns at exp2 1.43 ms.
 //
 // Codes are exact in fp16; scales stay out of the operands as in kv8_stream.cuh: the K scale multiplies the fp32 score,
 // the V scale is part of the exponent z = score + log2(v scale), and the sum of weights takes it out again.  The running
@@ -27,16 +26,14 @@
 #pragma once
 
 #include <cstddef>
-#include <type_traits>
 
 #include "kv8_append.cuh"
 #include "kv8_stream.cuh"
 
 namespace dkv {
 
-constexpr int kTileThreads = 768, kTileRows = 512, kTileKeys = 64, kTileCells = kTileKeys / kKv8CellKeys;
-constexpr int kTileStages = 4;       // of K and of V
-constexpr int kTileAhead = 2;        // key tiles in a converter's registers
+constexpr int kTileThreads = 512, kTileRows = 512, kTileKeys = 128, kTileCells = kTileKeys / kKv8CellKeys;
+constexpr int kTileStages = 3;       // of K and of V
 constexpr float kTileSlack = 8.0f;   // log2 of the most a weight may exceed 1 before the maximum is raised (fp16: 2^16)
 // Key tiles looked up at a time (a lane per cell), and how many such batches are kept.
 constexpr int kMetaBatch = 32 / kTileCells, kMetaBatches = 4, kMetaSlots = kMetaBatch * kMetaBatches;
@@ -45,7 +42,7 @@ struct __align__(16) TileMeta {  // of one key tile
   int64_t at[kTileCells];  // byte offset of a cell's K codes
   int key0[kTileCells];    // its first key
   float ks[kTileCells], lv[kTileCells], iv[kTileCells];  // K scale, log2 and inverse of the V scale
-  int there, last, pad[2];  // cells that are mapped; the last key, INT_MAX where the cells are not 64 mapped keys in a row
+  int there, last, pad[2];  // cells that are mapped; the last key, INT_MAX where the cells are not mapped keys in a row
 };
 
 // Bytes of a CTA's shared memory: 256 rows of Q, its halves of K and V as fp16.
@@ -58,11 +55,9 @@ struct TileSmem {
 
 struct TileBars {
   uint64_t meta_full[kMetaBatches], meta_empty[kMetaBatches];
-  // per row tile and S buffer, since S and the softmax may be two key tiles ahead of who waits for them:
-  uint64_t p_full[2][2];                             // of the pair, in the first CTA: both CTAs' softmax warps arrive
+  uint64_t p_full[2];                                // of the pair, in the first CTA: both CTAs' warps arrive
   uint64_t k_full[kTileStages], v_full[kTileStages];    // of each CTA's converters; in the first, the second's word too
-  uint64_t k_empty[kTileStages], v_empty[kTileStages], pv_done[2], o_full[2], drain;  // in both: the MMAs' commits arrive
-  uint64_t s_full[2][2];                             // in both
+  uint64_t k_empty[kTileStages], v_empty[kTileStages], s_full[2], o_full[2], drain;  // in both: the MMAs' commits arrive
 };
 constexpr int kTileBars = sizeof(TileBars) / 8;
 
@@ -167,43 +162,55 @@ __device__ __forceinline__ uint4 load_codes16(const uint8_t* p) {
   return w;
 }
 
-// A converter warp's share of a key tile in registers.  Of K: 16 rows (one cell) of the CTA's 32 keys, all dimensions; of V: 32
-// of the 64 keys, the CTA's half of the dimensions.
-template <int D, bool V>
+// A converter warp's share of a CTA's half of a key tile, in registers: K rows 64 rank + 16 warp .. + 15, all dimensions; V
+// rows 32 warp .. + 31, dimensions (d / 2) rank .. + d / 2.
+template <int D>
 struct TileCodes {
-  static constexpr int kLanes = V ? D / 32 : D / 16;  // of a row, 16 codes each
-  static constexpr int kRows = 32 / kLanes, kIters = (V ? 32 : 16) / kRows;
-  uint4 w[kIters];
+  static constexpr int kKLanes = D / 16, kKRows = 32 / kKLanes, kVLanes = D / 32, kVRows = 32 / kVLanes;
+  uint4 k[16 / kKRows], v[32 / kVRows];
 
-  // codes: of the K or V part; M's cell offsets are K's
-  __device__ __forceinline__ void load(const uint8_t* codes, const TileMeta& M, int rank, int sub, int lane) {
+  __device__ __forceinline__ void load_k(const uint8_t* codes, const TileMeta& M, int rank, int warp, int lane) {
+    const int cell = 4 * rank + warp;  // 16 rows of one cell
 #pragma unroll
-    for (int i = 0; i < kIters; ++i) {
-      const int r = i * kRows + lane / kLanes, cell = V ? 2 * sub + r / kKv8CellKeys : 2 * rank + sub;
-      w[i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < 16 / kKRows; ++i) {
+      k[i] = make_uint4(0u, 0u, 0u, 0u);
       if ((M.there >> cell) & 1)
-        w[i] = load_codes16(codes + M.at[cell] + (r % kKv8CellKeys) * D + (V ? rank * (D / 2) : 0) + (lane % kLanes) * 16);
+        k[i] = load_codes16(codes + M.at[cell] + (i * kKRows + lane / kKLanes) * D + (lane % kKLanes) * 16);
     }
   }
-  // V rows of no key, from T on, are stored as 0: weight 0 times them must stay 0, and e4m3 bytes may be NaN.
-  template <bool E4M3>
-  __device__ __forceinline__ void store(uint8_t* dst, const TileMeta& M, int T, int sub, int lane) const {
-    const int c = lane % kLanes;
+  __device__ __forceinline__ void load_v(const uint8_t* codes, const TileMeta& M, int rank, int warp, int lane) {
 #pragma unroll
-    for (int i = 0; i < kIters; ++i) {
-      const int r = (V ? 32 : 16) * sub + i * kRows + lane / kLanes;
-      if constexpr (V) {  // rows of d / 2 fp16: 128 or 64 bytes
-        uint4 x = w[i];
-        if (M.key0[r / kKv8CellKeys] + r % kKv8CellKeys >= T) x = make_uint4(0u, 0u, 0u, 0u);
-        store_codes<E4M3>(dst + r * D, 2 * c, D == 128 ? r & 7 : (r >> 1) & 3, 0, x);
-      } else {            // panels of 32 rows of 128 bytes
-        store_codes<E4M3>(dst + (c / 4) * (32 * 128) + r * 128, (c % 4) * 2, r & 7, c / 4, w[i]);
-      }
+    for (int i = 0; i < 32 / kVRows; ++i) {
+      const int r = 32 * warp + i * kVRows + lane / kVLanes, cell = r / kKv8CellKeys;
+      v[i] = make_uint4(0u, 0u, 0u, 0u);
+      if ((M.there >> cell) & 1)
+        v[i] = load_codes16(codes + M.at[cell] + (r % kKv8CellKeys) * D + rank * (D / 2) + (lane % kVLanes) * 16);
+    }
+  }
+  template <bool E4M3>
+  __device__ __forceinline__ void store_k(uint8_t* dst, int warp, int lane) const {  // panels of 64 rows of 128 bytes
+    const int c = lane % kKLanes;
+#pragma unroll
+    for (int i = 0; i < 16 / kKRows; ++i) {
+      const int r = 16 * warp + i * kKRows + lane / kKLanes;
+      store_codes<E4M3>(dst + (c / 4) * (64 * 128) + r * 128, (c % 4) * 2, r & 7, c / 4, k[i]);
+    }
+  }
+  // Rows of no key, from T on, are stored as 0: weight 0 times them must stay 0, and e4m3 bytes may be NaN.
+  template <bool E4M3>
+  __device__ __forceinline__ void store_v(uint8_t* dst, const TileMeta& M, int T, int warp, int lane) const {
+    const int c = lane % kVLanes;  // rows of d / 2 fp16: 128 or 64 bytes
+#pragma unroll
+    for (int i = 0; i < 32 / kVRows; ++i) {
+      const int r = 32 * warp + i * kVRows + lane / kVLanes;
+      uint4 x = v[i];
+      if (M.key0[r / kKv8CellKeys] + r % kKv8CellKeys >= T) x = make_uint4(0u, 0u, 0u, 0u);
+      store_codes<E4M3>(dst + r * D, 2 * c, D == 128 ? r & 7 : (r >> 1) & 3, 0, x);
     }
   }
 };
 
-// Softmax of a CTA's 128 rows of one row tile by eight warps, a thread half a row.  BIAS: scores may be capped or biased.
+// Softmax of a CTA's 128 rows of one row tile by four warps.  BIAS: scores may be capped or biased.
 template <int D, bool BIAS>
 struct TileSoftmax {
   const Kv8Attn& a;
@@ -211,10 +218,9 @@ struct TileSoftmax {
   const TileMeta* metas;
   TileBars* bars;
   volatile int* abort_flag;
-  uint32_t s_tmem, o_tmem;  // of this warp's lanes: the first S buffer, O
-  uint32_t p_full;          // cluster address of the pair's barrier of the first S buffer
-  float* tops;              // the row's maxima of this half; the other half's are 256 floats on or back
-  int tile, half, meet;     // meet: barrier of the two warps of the same rows
+  uint32_t s_tmem, o_tmem;  // of this warp's lanes
+  uint32_t p_full;          // cluster address of the pair's barrier
+  int tile;
   Kv8Row row;
   float scl, slope;  // row scale times the softmax scale (natural units); slope in log2 units
   float m, l;
@@ -261,11 +267,11 @@ struct TileSoftmax {
     }
   }
 
-  // The thread's scores in tensor memory as z, masked unless `whole`; returns their maximum.
-  __device__ __forceinline__ float transform(const TileMeta& M, uint32_t s_tmem, bool whole, bool behind, float two_over_cap, float per_cap) {
+  // The row's scores in tensor memory as z, masked unless `whole`; returns their maximum.
+  __device__ __forceinline__ float transform(const TileMeta& M, bool whole, bool behind, float two_over_cap, float per_cap) {
     float top = -INFINITY;
 #pragma unroll 1
-    for (int cell = 2 * half; cell < 2 * half + 2; ++cell) {
+    for (int cell = 0; cell < kTileCells; ++cell) {
       uint32_t r[16];
       tmem_ld_32x32b_x16(s_tmem + 16 * cell, r);
       tmem_ld_wait();
@@ -295,64 +301,56 @@ struct TileSoftmax {
   }
 
   __device__ __forceinline__ bool run(int n) {
-    const float two_over_cap = BIAS && a.softcap > 0.f ? 2.0f * kLog2e / a.softcap : 0.f;
-    const float per_cap = BIAS && a.softcap > 0.f ? 1.0f / a.softcap : 0.f;
     const float scl2 = scl * kLog2e;
+    const float per_cap = BIAS && a.softcap > 0.f ? 1.0f / a.softcap : 0.f;
     const bool behind = BIAS && __all_sync(~0u, slope == 0.f || seq.prefix <= row.pos + 1);
-    bool ok = true;  // no wait of this warp has run out; both warps of a row leave together, at the barrier where they meet
+    const float two_over_cap = BIAS && a.softcap > 0.f ? 2.0f * kLog2e / a.softcap : 0.f;
     for (int j = 0; j < n; ++j) {
+      bool ok = true;
       if (j % kMetaBatch == 0)
-        ok = ok && mbar_wait(smem_u32(&bars->meta_full[j / kMetaBatch % kMetaBatches]), (j / kMetaSlots) & 1, abort_flag);
-      ok = __all_sync(~0u, ok && mbar_wait(smem_u32(&bars->s_full[tile][j & 1]), (j >> 1) & 1, abort_flag));
+        ok = mbar_wait(smem_u32(&bars->meta_full[j / kMetaBatch % kMetaBatches]), (j / kMetaSlots) & 1, abort_flag);
+      if (!__all_sync(~0u, ok && mbar_wait(smem_u32(&bars->s_full[tile]), j & 1, abort_flag))) return false;
       tc_fence_after();
       const TileMeta& M = metas[j % kMetaSlots];
-      const uint32_t sb = s_tmem + kTileKeys * (j & 1);
       // whole: every key of the tile is seen by all of the warp's rows
       const bool whole = __all_sync(~0u, row.lo <= M.key0[0] && M.last <= row.hi);
-      const float2 ks = reinterpret_cast<const float2*>(M.ks)[half], lv = reinterpret_cast<const float2*>(M.lv)[half];
-      const float kk[2] = {ks.x * scl2, ks.y * scl2};
-      uint32_t r[32];
       // raw: without a bias z is one fused multiply-add of the raw score, done again in the second pass.  m then is not
       // the exact maximum of those sums, but within a rounding of it, so scores whose rounding is not small against 1 take
-      // the other path: z made cell by cell in tensor memory.
+      // the other path: z made cell by cell in tensor memory, by a loop (unrolled code for all of them evicted the warps'
+      // other programs from the instruction caches).
+      uint32_t r[4][32];
       bool raw = !BIAS && whole;
       float top = -INFINITY;
       if (raw) {
-        tmem_ld_32x32b_x32(sb + 32 * half, r);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(s_tmem + 32 * c, r[c]);
         tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
+        for (int cell = 0; cell < kTileCells; ++cell) {
+          const uint32_t* x = &r[cell / 2][16 * (cell % 2)];
           float y[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t* x = &r[16 * e + 4 * i];
-            y[i] = fmaxf(fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])), fmaxf(__uint_as_float(x[2]), __uint_as_float(x[3])));
-          }
-          top = fmaxf(top, fmaf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), kk[e], e ? lv.y : lv.x));
+          for (int i = 0; i < 4; ++i)
+            y[i] = fmaxf(fmaxf(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1])),
+                         fmaxf(__uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3])));
+          top = fmaxf(top, fmaf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), M.ks[cell] * scl2, M.lv[cell]));
         }
         raw = __all_sync(~0u, fabsf(top) < 65536.0f);
       }
       if (!raw) {
-        top = transform(M, sb, whole, behind, two_over_cap, per_cap);
-        tmem_ld_32x32b_x32(sb + 32 * half, r);
+        top = transform(M, whole, behind, two_over_cap, per_cap);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(s_tmem + 32 * c, r[c]);
         tmem_ld_wait();
       }
-      // the row's maximum of both halves; both warps have read their scores
-      tops[512 * (j & 1)] = top;
-      tc_fence_before();
-      if (named_bar_or(meet, 64, !ok)) return false;
-      tc_fence_after();
-      top = fmaxf(top, tops[512 * (j & 1) + (half ? -256 : 256)]);
-      const bool rise = top > m + kTileSlack, any = __any_sync(~0u, rise);
-      if (any) {
+      const bool rise = top > m + kTileSlack;
+      if (__any_sync(~0u, rise)) {
         const float now = rise ? top : m, fix = fast_exp2(m - now);
         m = now;
         l *= fix;
         if (j > 0) {
-          ok = __all_sync(~0u, mbar_wait(smem_u32(&bars->pv_done[tile]), (j - 1) & 1, abort_flag));
-          tc_fence_after();
 #pragma unroll 1
-          for (int c = half * (D / 32); c < (half + 1) * (D / 32); ++c) {
+          for (int c = 0; c < D / 16; ++c) {
             uint32_t x[16];
             tmem_ld_32x32b_x16(o_tmem + 16 * c, x);
             tmem_ld_wait();
@@ -362,37 +360,40 @@ struct TileSoftmax {
           }
         }
       }
-      const float2 iv = reinterpret_cast<const float2*>(M.iv)[half];
-      uint32_t p[16];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float mul = raw ? kk[e] : 1.0f, add = raw ? (e ? lv.y : lv.x) - m : -m;
-        const uint64_t mul_2 = pack2(mul, mul), add_2 = pack2(add, add);
-        uint64_t sum2 = 0;
-        float x, y;
+      for (int c = 0; c < 4; ++c) {
+        uint32_t p[16];
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-          const uint32_t* q = &r[16 * e + i];
-          unpack2(fma2(pack2(__uint_as_float(q[0]), __uint_as_float(q[1])), mul_2, add_2), x, y);
-          x = fast_exp2(x), y = fast_exp2(y);
-          sum2 = add2(sum2, pack2(x, y));
-          p[8 * e + i / 2] = pack_f16(x, y);
+        for (int gq = 0; gq < 2; ++gq) {
+          const int cell = 2 * c + gq;
+          const float kk = raw ? M.ks[cell] * scl2 : 1.0f, add = raw ? M.lv[cell] - m : -m;
+          const uint64_t kk2 = pack2(kk, kk), add_2 = pack2(add, add);
+          uint64_t sum2 = 0;
+#pragma unroll
+          for (int i = 0; i < 16; i += 2) {
+            float x, y;
+            unpack2(fma2(pack2(__uint_as_float(r[c][gq * 16 + i]), __uint_as_float(r[c][gq * 16 + i + 1])), kk2, add_2), x, y);
+            x = fast_exp2(x), y = fast_exp2(y);
+            sum2 = add2(sum2, pack2(x, y));
+            p[gq * 8 + i / 2] = pack_f16(x, y);
+          }
+          float x, y;
+          unpack2(sum2, x, y);
+          x += y;
+          if (x != 0.f) l = fmaf(x, M.iv[cell], l);  // a cell out of sight adds nothing, even where its scale is NaN
         }
-        unpack2(sum2, x, y);
-        x += y;
-        if (x != 0.f) l = fmaf(x, e ? iv.y : iv.x, l);  // a cell out of sight adds nothing, even where its scale is NaN
+        tmem_st_32x32b_x16(s_tmem + 16 * c, p);
       }
-      tmem_st_32x32b_x16(sb + 16 * half, p);  // over scores of the first half, which both warps have read
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane_id() == 0) {
-        mbar_arrive_remote(p_full + 8 * (j & 1));
+        mbar_arrive_remote(p_full);
         if (j % kMetaBatch == kMetaBatch - 1)
           mbar_arrive(smem_u32(&bars->meta_empty[j / kMetaBatch % kMetaBatches]));
       }
     }
-    return ok;
+    return true;
   }
 };
 
@@ -404,7 +405,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
   __shared__ __align__(8) TileBars bars;
   __shared__ TileMeta metas[kMetaSlots];
   __shared__ float qscale[256];
-  __shared__ float tops[2 * 512];  // two key tiles in turn: maxima of 256 rows' first halves, of their second halves
   __shared__ uint32_t tmem_base;
   __shared__ int abort_flag;
   uint8_t* smem = align_shared<1024>(smem_raw);
@@ -431,12 +431,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
   if (threadIdx.x == 0) {
     abort_flag = 0;
     const uint32_t b = smem_u32(&bars);
-    constexpr int kP = 2 * kMetaBatches, kFull = kP + 4, kRest = kFull + 2 * kTileStages;
-    for (int i = 0; i < kTileBars; ++i)  // meta_empty: the CTA's warps that read a batch
-      mbar_init(b + 8 * i, i < kMetaBatches ? 1 : i < kP ? 8 * tiles + 4 : i < kFull ? 16 : i < kRest ? (rank == 0 ? 3 : 2) : 1);
+    constexpr int kP = 2 * kMetaBatches, kFull = kP + 2, kRest = kFull + 2 * kTileStages;
+    for (int i = 0; i < kTileBars; ++i)  // meta_empty: the CTA's warps that read the scales
+      mbar_init(b + 8 * i, i < kMetaBatches ? 1 : i < kP ? 4 * tiles + 4 : i < kFull ? 8 : i < kRest ? (rank == 0 ? 5 : 4) : 1);
     fence_barrier_init();
   }
-  if (warp == 20) {
+  if (warp == 12) {
     tmem_alloc_pair(smem_u32(&tmem_base), 512);
     tmem_relinquish_pair();
   }
@@ -506,56 +506,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     const uint32_t q_lo = desc_lo(sb + L::q), k_lo = desc_lo(sb + L::k), v_lo = desc_lo(sb + L::v);
     constexpr uint32_t kKFull = offsetof(TileBars, k_full), kVFull = offsetof(TileBars, v_full),
                        kKEmpty = offsetof(TileBars, k_empty), kVEmpty = offsetof(TileBars, v_empty),
-                       kPFull = offsetof(TileBars, p_full),
-                       kSFull = offsetof(TileBars, s_full), kPvDone = offsetof(TileBars, pv_done), kOFull = offsetof(TileBars, o_full),
-                       kDrain = offsetof(TileBars, drain);
+                       kPFull = offsetof(TileBars, p_full), kSFull = offsetof(TileBars, s_full),
+                       kOFull = offsetof(TileBars, o_full), kDrain = offsetof(TileBars, drain);
     auto wait_pair = [&](uint32_t b, uint32_t par) { return __all_sync(~0u, mbar_wait_cluster(b, par, &abort_flag)) != 0; };
     auto wait = [&](uint32_t b, uint32_t par) { return __all_sync(~0u, mbar_wait(b, par, &abort_flag)) != 0; };
-    auto scores = [&](int t, int st, uint32_t buf) {
+    auto scores = [&](int t, int st) {
       const uint32_t qa = q_lo + t * (L::kQ / 16), ka = k_lo + st * (L::kHalf / 16);
 #pragma unroll
       for (int i = 0; i < D / 16; ++i)
-        umma_f16_ss_pair<kHiK, kHiK, kIdS>(tm + 2 * kTileKeys * t + kTileKeys * buf, qa + ((i / 4) * (128 * 128) + (i % 4) * 32) / 16,
-                                           ka + ((i / 4) * (32 * 128) + (i % 4) * 32) / 16, i > 0, on);
-      umma_commit_both(bar + kSFull + 8 * (2 * t + buf), on);
+        umma_f16_ss_pair<kHiK, kHiK, kIdS>(tm + 128 * t, qa + ((i / 4) * (128 * 128) + (i % 4) * 32) / 16,
+                                           ka + ((i / 4) * (64 * 128) + (i % 4) * 32) / 16, i > 0, on);
+      umma_commit_both(bar + kSFull + 8 * t, on);
     };
     bool ok = wait_pair(bar + kKFull, 0);
     if (ok) {
       tc_fence_after();
-      scores(0, 0, 0);
-      if (num_t > 1) scores(1, 0, 0);
+      scores(0, 0);
+      if (num_t > 1) scores(1, 0);
       umma_commit_both(bar + kKEmpty, on);
     }
     int st = 0, nx = 1 % kTileStages;     // stage of key tile j and of j + 1
     uint32_t st_par = 0, nx_par = 0, par = 0;
     for (int j = 0; ok && j < num; ++j) {
-      if (j + 1 < num) {
-        if (!(ok = wait_pair(bar + kKFull + 8 * nx, nx_par))) break;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (!ok || t >= num_t) break;
-          // S goes over the P that the MMAs of key tile j - 1 read: MMAs of different shapes keep no order by themselves
-          if (j > 0 && !(ok = wait(bar + kPvDone + 8 * t, par ^ 1))) break;
-          tc_fence_after();
-          scores(t, nx, par ^ 1);
-        }
-        if (!ok) break;
-        umma_commit_both(bar + kKEmpty + 8 * nx, on);
-      }
-      // what p_full hands over lies in tensor memory, ordered by the tcgen05 fences around the barrier
-      ok = wait_pair(bar + kVFull + 8 * st, st_par);
+      const bool more = j + 1 < num;
+      ok = wait_pair(bar + kVFull + 8 * st, st_par) && (!more || wait_pair(bar + kKFull + 8 * nx, nx_par));
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         if (!ok || t >= num_t) break;
-        if (!(ok = wait(bar + kPFull + 8 * (2 * t + par), (j >> 1) & 1))) break;
+        // what p_full hands over lies in tensor memory, ordered by the tcgen05 fences around the barrier
+        if (!(ok = wait(bar + kPFull + 8 * t, par))) break;
         tc_fence_after();
         const uint32_t va = v_lo + st * (L::kHalf / 16);
 #pragma unroll
         for (int i = 0; i < kTileKeys / 16; ++i)
-          umma_f16_ts_pair<kHiV, kIdO>(tm + 256 + D * t, tm + 2 * kTileKeys * t + kTileKeys * par + 8 * i, va + i * D, i > 0 ? 1 : j, on);
-        umma_commit_both(bar + (j + 1 < num ? kPvDone : kOFull) + 8 * t, on);
+          umma_f16_ts_pair<kHiV, kIdO>(tm + 256 + D * t, tm + 128 * t + 8 * i, va + i * D, i > 0 ? 1 : j, on);
+        if (more) scores(t, nx);
+        else umma_commit_both(bar + kOFull + 8 * t, on);
       }
-      if (ok) umma_commit_both(bar + kVEmpty + 8 * st, on);
+      if (ok) {
+        umma_commit_both(bar + kVEmpty + 8 * st, on);
+        if (more) umma_commit_both(bar + kKEmpty + 8 * nx, on);
+      }
       par ^= 1;
       st = nx, st_par = nx_par;
       if (++nx == kTileStages) nx = 0, nx_par ^= 1;
@@ -566,7 +557,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
   };
   auto look_up = [&]() {
     for (int b = 0; b * kMetaBatch < n; ++b) {
-      // a lane per cell; tiles go from the nearest keys to the farthest
+      // lane: cell lane % 8 of key tile 4 b + lane / 8; tiles go from the nearest keys to the farthest
       const int j = b * kMetaBatch + lane / kTileCells, v = v0 + (n - 1 - j) * kTileCells + lane % kTileCells;
       int key0 = INT_MAX / 2;
       int64_t at = -1;
@@ -598,41 +589,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
       if (lane == 0) mbar_arrive(smem_u32(&bars.meta_full[b % kMetaBatches]));
     }
   };
-  // K or V: `sub` is the warp's number among the two
-  auto convert = [&](auto part, uint32_t smem_at, uint64_t* full, uint64_t* empty, int sub) {
-    constexpr bool V = decltype(part)::value;
-    TileCodes<D, V> x[kTileAhead];
-    const uint8_t* codes = a.codes + (V ? static_cast<int64_t>(a.block) * D : 0);
-    bool ok = true;
-    auto load = [&](int j, TileCodes<D, V>& c) {
-      if (j % kMetaBatch == 0)
-        ok = ok && __all_sync(~0u, mbar_wait(smem_u32(&bars.meta_full[j / kMetaBatch % kMetaBatches]),
-                                             (j / kMetaSlots) & 1, &abort_flag));
-      if (ok) c.load(codes, metas[j % kMetaSlots], rank, sub, lane);
-    };
-#pragma unroll
-    for (int i = 0; i < kTileAhead; ++i)
-      if (i < n) load(i, x[i]);
-    int st = 0;
-    uint32_t par = 1;
-    for (int j = 0; ok && j < n; j += kTileAhead) {
-#pragma unroll
-      for (int i = 0; i < kTileAhead; ++i) {
-        if (!ok || j + i >= n) break;
-        if (!(ok = __all_sync(~0u, mbar_wait(smem_u32(empty + st), par, &abort_flag)))) break;
-        x[i].template store<E4M3>(smem + smem_at + st * L::kHalf, metas[(j + i) % kMetaSlots], seq.T, sub, lane);
+  auto convert = [&]() {
+    TileCodes<D> x;
+    const int w = warp - 8;
+    const uint8_t* vcodes = a.codes + static_cast<int64_t>(a.block) * D;
+    for (int j = 0; j <= n; ++j) {  // stores key tile j - 1, loads j
+      if (j < n && j % kMetaBatch == 0 &&
+          !__all_sync(~0u, mbar_wait(smem_u32(&bars.meta_full[j / kMetaBatch % kMetaBatches]),
+                                     (j / kMetaSlots) & 1, &abort_flag)))
+        break;
+      const TileMeta &last = metas[(j + kMetaSlots - 1) % kMetaSlots], &next = metas[j % kMetaSlots];
+      const int st = (j + kTileStages - 1) % kTileStages;
+      const uint32_t free_par = (((j - 1) / kTileStages) & 1) ^ 1;
+      if (j > 0) {
+        if (!__all_sync(~0u, mbar_wait(smem_u32(&bars.k_empty[st]), free_par, &abort_flag))) break;
+        x.template store_k<E4M3>(smem + L::k + st * L::kHalf, w, lane);
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&bars.k_full[st]));
+      }
+      if (j < n) x.load_k(a.codes, next, rank, w, lane);
+      if (j > 0) {
+        if (!__all_sync(~0u, mbar_wait(smem_u32(&bars.v_empty[st]), free_par, &abort_flag))) break;
+        x.template store_v<E4M3>(smem + L::v + st * L::kHalf, last, seq.T, w, lane);
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive(smem_u32(full + st));
-          if ((j + i) % kMetaBatch == kMetaBatch - 1)
-            mbar_arrive(smem_u32(&bars.meta_empty[(j + i) / kMetaBatch % kMetaBatches]));
+          mbar_arrive(smem_u32(&bars.v_full[st]));
+          if ((j - 1) % kMetaBatch == kMetaBatch - 1)
+            mbar_arrive(smem_u32(&bars.meta_empty[(j - 1) / kMetaBatch % kMetaBatches]));
         }
-        if (++st == kTileStages) st = 0, par ^= 1;
-        if (j + i + kTileAhead < n) load(j + i + kTileAhead, x[i]);
       }
+      if (j < n) x.load_v(vcodes, next, rank, w, lane);
     }
   };
+
   auto pass_on = [&](uint64_t* full) {  // one thread of the second CTA
     for (int j = 0; j < n; ++j) {
       const uint32_t bar = smem_u32(full + j % kTileStages);
@@ -641,32 +632,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     }
   };
 
-  // per sub-partition: 4 x 80 + 104 + 56 = 6 x 80 registers a thread, what the CTA was launched with
-  if (warp < 16) {
-    const int tile = (warp / 4) & 1, half = warp / 8;
+  // per sub-partition: 2 x 184 + 96 + 48 = 4 x 128 registers a thread, what the CTA was launched with
+  if (warp < 8) {
+    regs_take<184>();
+    const int tile = warp / 4;
     if (tile < tiles) {
       const uint32_t lanes = static_cast<uint32_t>(warp % 4) << 21;  // (32 * quarter) << 16
       const int r = tile * 128 + (warp % 4) * 32 + lane, rr = min(global_row(r), r1 - 1);
       const bool mine = global_row(r) < r1;
-      TileSoftmax<D, BIAS> sm{a, seq, metas, &bars, &abort_flag, (tmem + 2 * kTileKeys * tile) | lanes,
-                              (tmem + 256 + D * tile) | lanes, mapa_shared(smem_u32(&bars.p_full[tile][0]), 0),
-                              tops + 256 * half + r, tile, half, 1 + warp % 8,
+      TileSoftmax<D, BIAS> sm{a, seq, metas, &bars, &abort_flag, (tmem + 128 * tile) | lanes,
+                              (tmem + 256 + D * tile) | lanes, mapa_shared(smem_u32(&bars.p_full[tile]), 0), tile,
                               kv8_row(a, seq, rr / a.group), mine ? qscale[r] : 0.f,
                               a.slopes ? a.slopes[h * a.group + rr % a.group] * kLog2e : 0.f, kNoMax, 0.f};
       bool ok = sm.run(n);
-      // not pv_done, of which up to two phases may be open or done here
       if (ok && n > 0) ok = __all_sync(~0u, mbar_wait(smem_u32(&bars.o_full[tile]), 0, &abort_flag));
       tc_fence_after();
-      // the row's sum of both halves
-      named_bar_sync(1 + warp % 8, 64);
-      sm.tops[0] = sm.l;
-      named_bar_sync(1 + warp % 8, 64);
-      const float sum = ok ? sm.l + sm.tops[half ? -256 : 256] : NAN;
+      const float sum = ok ? sm.l : NAN;
       const float inv = a.nsplit > 1 ? 1.0f : (sum == 0.f ? 0.f : 1.0f / sum);
       const int64_t at = static_cast<int64_t>(seq.q0 + rr / a.group) * hq + h * a.group + rr % a.group;
       const int64_t prow = split * (a.total_q * hq) + at;
 #pragma unroll
-      for (int c = half * (D / 64); c < (half + 1) * (D / 64); ++c) {
+      for (int c = 0; c < D / 32; ++c) {
         uint32_t x[32];
         if (n > 0) {
           tmem_ld_32x32b_x32(sm.o_tmem + 32 * c, x);
@@ -698,26 +684,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
           }
         }
       }
-      if (mine && half == 0) {
+      if (mine) {
         if (a.nsplit > 1) a.ml[prow] = make_float2(sm.m, sum);
         else if (a.lse) a.lse[at] = sum == 0.f ? -INFINITY : (sm.m + log2f(sum)) * kLn2;
       }
       tc_fence_before();
     }
-  } else if (warp < 20) {
-    regs_take<104>();
-    if (warp < 18) convert(std::false_type(), L::k, bars.k_full, bars.k_empty, warp - 16);
-    else convert(std::true_type(), L::v, bars.v_full, bars.v_empty, warp - 18);
+  } else if (warp < 12) {
+    regs_give<96>();
+    convert();
   } else {
-    regs_give<56>();
-    if (warp == 20 && rank == 0 && n > 0) issue_mmas();
-    if (warp >= 22 && lane == 0 && rank == 1) pass_on(warp == 22 ? bars.k_full : bars.v_full);
+    regs_give<48>();
+    if (warp == 12 && rank == 0 && n > 0) issue_mmas();
+    if (warp >= 14 && lane == 0 && rank == 1) pass_on(warp == 14 ? bars.k_full : bars.v_full);
     __syncwarp();
-    if (warp == 21) look_up();
+    if (warp == 13) look_up();
   }
   __syncthreads();
   cluster_sync_all();  // neither CTA leaves while the other's MMAs, commits or arrivals may reach it
-  if (warp == 20) {
+  if (warp == 12) {
     tc_fence_after();
     tmem_dealloc_pair(tmem, 512);
   }
