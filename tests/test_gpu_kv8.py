@@ -416,6 +416,74 @@ def test_attention_twice_is_bit_identical_and_no_sequences_is_a_no_op():
     D.deltakv_kv8_append(shape, cache, empty[:, :2], empty[:, :2], _i32([0]), _i32([]), table[:0].cuda(), 1)
 
 
+@pytest.mark.parametrize("hq,hkv,d,B,code,softcap", [(16, 4, 128, 16, "e4m3", 0.0), (16, 4, 128, 16, "e4m3", 50.0),
+                                                     (8, 2, 64, 64, "int8", 0.0)])
+def test_long_prompts_over_and_over(hq, hkv, d, B, code, softcap):
+    """Many waves of CTAs of the tcgen05 kernel, twenty times: every wait is met (the device error word stays 0) and every
+    run gives the same bits; rows far apart are checked against fp64."""
+    shape, T = D.KV8Shape(hq, hkv, d, B, BF, code), 6000
+    g = _gen(41)
+    codes, scales, table = K.cache_for(shape, [T], g)
+    q = torch.randn(T, hq, d, generator=g).to(BF)
+    cache = D.KV8Cache(codes.view(torch.uint8).cuda().view(shape.code_dtype), scales.cuda())
+    ws = D.alloc_workspace(D.kv8_attention_workspace(shape, 1, T, T, T))
+    dq, cu, ctx, tab = q.cuda(), _i32([0, T]), _i32([T]), table.cuda()
+    first = None
+    for _ in range(20):
+        out, lse = torch.empty_like(dq), torch.empty(T, hq, device="cuda")
+        D.deltakv_kv8_attention(shape, cache, dq, cu, ctx, tab, T, T, out, lse, ws, softcap=softcap)
+        assert D.deltakv_get_device_error() == 0
+        first = first or (out, lse)
+        assert torch.equal(out, first[0]) and torch.equal(lse, first[1])
+    for p in (0, 1, 129, 2047, 4444, T - 1):  # a row is the last token of a shorter sequence in the same blocks
+        ro, rl, to, tl = K.attention(shape, codes, scales, table, q[p:p + 1], [0, 1], [p + 1], softcap=softcap)
+        K.check(first[0][p:p + 1], ro, to, "out")
+        K.check(first[1][p:p + 1], rl, tl, "lse")
+
+
+def test_two_graphs_share_a_workspace_and_two_streams_do_not():
+    """Graphs of different shapes that use one workspace, replayed in turn, and calls on two streams with a workspace each."""
+    g = _gen(43)
+    shape = D.KV8Shape(8, 2, 128, 16, BF, "int8")
+    ctx = [5000, 3000]
+    codes, scales, table = K.cache_for(shape, ctx, g)
+    cache = D.KV8Cache(codes.cuda(), scales.cuda())
+    dctx, tab = _i32(ctx), table.cuda()
+    sizes = (1, 2, 40)
+    q = {n: torch.randn(2 * n, 8, 128, generator=g).to(BF) for n in sizes}
+    ws = D.alloc_workspace(max(D.kv8_attention_workspace(shape, 2, 2 * n, n, 5000) for n in sizes)).fill_(0xff)
+    ref = {n: K.attention(shape, codes, scales, table, q[n], [0, n, 2 * n], ctx) for n in sizes}
+
+    def call(n, out, lse, work, stream=None):
+        D.deltakv_kv8_attention(shape, cache, dq[n], cus[n], dctx, tab, n, 5000, out, lse,
+                                work, stream=stream)
+
+    dq, cus = {n: q[n].cuda() for n in sizes}, {n: _i32([0, n, 2 * n]) for n in sizes}
+    outs = {n: (torch.empty_like(dq[n]), torch.empty(2 * n, 8, device="cuda")) for n in sizes}
+    graphs = {}
+    for n in sizes:
+        graphs[n] = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graphs[n]):
+            call(n, *outs[n], ws)
+    for _ in range(3):
+        for n in sizes:
+            graphs[n].replay()
+    torch.cuda.synchronize()
+    for n in sizes:
+        K.check(outs[n][0], ref[n][0], ref[n][2], "out")
+        K.check(outs[n][1], ref[n][1], ref[n][3], "lse")
+    streams = [torch.cuda.Stream() for _ in sizes]
+    own = [D.alloc_workspace(D.kv8_attention_workspace(shape, 2, 2 * n, n, 5000)) for n in sizes]
+    two = {n: (torch.empty_like(dq[n]), torch.empty(2 * n, 8, device="cuda")) for n in sizes}
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for n, st, w in zip(sizes, streams, own):
+            call(n, *two[n], w, st)
+    torch.cuda.synchronize()
+    for n in sizes:
+        assert torch.equal(two[n][0], outs[n][0]) and torch.equal(two[n][1], outs[n][1])
+
+
 # ------------------------------------------------------------------------------------------------------------------
 # merge
 # ------------------------------------------------------------------------------------------------------------------
