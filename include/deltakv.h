@@ -322,7 +322,7 @@ dkv_status deltakv_decode_attention_noalloc(const dkv_shape* shape, const dkv_pa
  *
  * Layout (one dkv_kv8_cache per layer; B = block_tokens, d = head_dim):
  *   codes   [num_blocks][H_kv][2][B][d]  8-bit codes of K (index 0) and V (index 1)
- *   scales  [num_blocks][H_kv][2]        float32; a value is code * scale
+ *   scales  [num_blocks][H_kv][2]        float32, positive (append writes no others, or NaN); a value is code * scale
  * Block tables are those of the compressed cache: logical block b holds positions bB .. bB+B-1.
  *
  * Codes: DKV_KV8_INT8 two's complement in [-127, 127]; DKV_KV8_E4M3 OCP 8-bit floats (4 exponent bits, no
@@ -371,7 +371,7 @@ typedef struct dkv_kv8_rope {
  *     s = cap(softmax_scale q.k_t) - slope_h |p - t|,    cap(x) = softcap tanh(x / softcap)  (softcap > 0)
  * and is seen iff  t < T,  (t <= p and (window == 0 or p - t < window)) or t < prefix_len,  and t >= first_key. */
 typedef struct dkv_kv8_score {
-  float softcap;                /* 0: none                                                                   */
+  float softcap;                /* 0: none; else 1e-6 .. 1e30                                                */
   int32_t window;               /* 0: none                                                                   */
   const float* alibi_slopes;    /* [H_q] distance bias (device) or NULL                                      */
   const int32_t* prefix_lens;   /* [num_seqs] keys below it are seen by every query: a bidirectional prefix, or
@@ -417,7 +417,8 @@ dkv_status deltakv_kv8_attention_workspace(const dkv_kv8_shape* shape, int32_t n
  *   q             query row i, head h at q + i * q_stride + h * d (stride in elements, a multiple of 16 bytes)
  *   cu_q          [num_seqs+1] int32 prefix sums of the query tokens, or NULL: one per sequence (total_q = num_seqs)
  *   context_lens  [num_seqs] int32, 0 <= T <= max_ctx, the query tokens among them
- *   block_tables  [num_seqs][max_blocks] int32; blocks that no query sees need not be mapped
+ *   block_tables  [num_seqs][max_blocks] int32; blocks outside the range of keys that a sequence's queries see (before
+ *                 the window and behind the prefix, behind the context) need not be mapped
  *   total_q, max_q, max_ctx  host-side bounds: query rows; most query tokens of one sequence; longest context
  *   softmax_scale <= 0 selects 1/sqrt(d)
  *   out           [total_q][H_q][d] dtype;  lse [total_q][H_q] float32 or NULL.  Rows of no sequence stay as they were

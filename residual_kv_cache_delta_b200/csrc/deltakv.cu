@@ -499,7 +499,7 @@ dkv_status deltakv_kv8_attention_workspace(const dkv_kv8_shape* s, int32_t num_s
   if (st != DKV_OK) return st;
   if (bytes == nullptr) return DKV_ERR_INVALID_ARG;
   if ((st = check_kv8_bounds(s, num_seqs, total_q, max_q, max_ctx)) != DKV_OK) return st;
-  *bytes = dkv::kv8_attn_layout(*s, dkv::kv8_attn_splits(*s, num_seqs, total_q, max_q, max_ctx), total_q).total;
+  *bytes = dkv::kv8_attn_layout(*s, dkv::kv8_attn_splits(*s, num_seqs, max_q, max_ctx), total_q).total;
   return DKV_OK;
 }
 
@@ -511,7 +511,8 @@ dkv_status deltakv_kv8_attention(const dkv_kv8_shape* shape, const dkv_kv8_cache
   dkv_status st = check_kv8(shape);
   if (st != DKV_OK) return st;
   if (cache == nullptr || max_blocks < 0) return DKV_ERR_INVALID_ARG;
-  if (score != nullptr && (!(score->softcap >= 0.0f) || score->softcap > 3.402823466e38f || score->window < 0))
+  if (score != nullptr && (!(score->softcap >= 0.0f) || score->softcap > 1e30f ||
+                           (score->softcap > 0.0f && score->softcap < 1e-6f) || score->window < 0))
     return DKV_ERR_INVALID_ARG;
   if (softmax_scale != softmax_scale) return DKV_ERR_INVALID_ARG;
   if ((st = check_kv8_bounds(shape, num_seqs, total_q, max_q, max_ctx)) != DKV_OK) return st;
@@ -522,7 +523,7 @@ dkv_status deltakv_kv8_attention(const dkv_kv8_shape* shape, const dkv_kv8_cache
   if (!kv8_rows_ok(shape, q, q_stride, shape->num_q_heads) || !aligned16(out)) return DKV_ERR_INVALID_ARG;
   if ((st = check_kv8_cache(shape, cache)) != DKV_OK) return st;
   const dkv::Kv8AttnWs w =
-      dkv::kv8_attn_layout(*shape, dkv::kv8_attn_splits(*shape, num_seqs, total_q, max_q, max_ctx), total_q);
+      dkv::kv8_attn_layout(*shape, dkv::kv8_attn_splits(*shape, num_seqs, max_q, max_ctx), total_q);
   if (w.total > 0) {
     if (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return DKV_ERR_INVALID_ARG;
     if (workspace_bytes < w.total) return DKV_ERR_WORKSPACE;

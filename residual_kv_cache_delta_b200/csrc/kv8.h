@@ -71,7 +71,7 @@ inline Kv8AttnWs kv8_attn_layout(const dkv_kv8_shape& sh, int nsplit, int64_t to
 }
 
 dkv_status launch_kv8_append(const Kv8AppendArgs& a, cudaStream_t st);
-int kv8_attn_splits(const dkv_kv8_shape& sh, int num_seqs, int64_t total_q, int max_q, int max_ctx);
+int kv8_attn_splits(const dkv_kv8_shape& sh, int num_seqs, int max_q, int max_ctx);
 dkv_status launch_kv8_attention(const Kv8AttnArgs& a, const Kv8AttnWs& w, void* workspace, cudaStream_t st);
 dkv_status launch_merge(int dtype, int64_t rows, int head_dim, int n, const void* const* outs,
                         const float* const* lses, void* out, float* lse, cudaStream_t st);

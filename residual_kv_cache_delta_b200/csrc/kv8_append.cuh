@@ -246,7 +246,7 @@ __global__ void __maxnreg__(80) kv8_append_kernel(const __grid_constant__ Kv8App
   const int row0 = a.cu_new[s], n = a.cu_new[s + 1] - row0, start = a.start_pos[s];
   if (n <= 0) return;
   if (row0 < 0 || n > a.max_new || static_cast<int64_t>(row0) + n > a.total_new || start < 0 ||
-      start > INT32_MAX - n) {
+      start > INT32_MAX - 64 - n) {  // positions of a block's rows fit an int
     if (threadIdx.x == 0) record_error(DKV_DEVERR_BOUNDS);
     return;
   }

@@ -42,7 +42,7 @@ static Kv8Plan kv8_plan(const dkv_kv8_shape& sh, int num_seqs, int max_q, int sp
   return p;
 }
 
-int kv8_attn_splits(const dkv_kv8_shape& sh, int num_seqs, int64_t total_q, int max_q, int max_ctx) {
+int kv8_attn_splits(const dkv_kv8_shape& sh, int num_seqs, int max_q, int max_ctx) {
   return kv8_plan(sh, num_seqs, max_q, max_ctx).nsplit;
 }
 
@@ -120,11 +120,12 @@ dkv_status launch_kv8_attention(const Kv8AttnArgs& a, const Kv8AttnWs& w, void* 
   p.total_q = a.total_q, p.max_q = a.max_q, p.max_ctx = a.max_ctx;
   p.scale = a.softmax_scale > 0.f ? a.softmax_scale : 1.0f / sqrtf(static_cast<float>(sh.head_dim));
   if (a.score) {
-    p.softcap = a.score->softcap, p.window = a.score->window, p.slopes = a.score->alibi_slopes;
+    // a window of at least the longest context hides nothing
+    p.softcap = a.score->softcap, p.window = a.score->window < a.max_ctx ? a.score->window : 0, p.slopes = a.score->alibi_slopes;
     p.prefix_lens = a.score->prefix_lens, p.first_key = a.score->first_key;
   }
   p.out = a.out, p.lse = a.lse, p.nsplit = w.nsplit;
-  if (p.window > 0 && p.window < a.max_ctx)  // fewer keys to share out than the workspace was sized for
+  if (p.window > 0)  // fewer keys to share out than the workspace was sized for
     p.nsplit = std::min(p.nsplit, kv8_plan(sh, a.num_seqs, a.max_q, static_cast<int>(std::min<int64_t>(
                                                a.max_ctx, int64_t{a.max_q} + p.window))).nsplit);
   p.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + w.ml);

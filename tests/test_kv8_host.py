@@ -102,7 +102,8 @@ def test_attention_refusals(lib):
                 dict(cu=0, total=1, max_q=0)):
         assert attend(lib, **bad) == ARG, bad
     score = lambda **kw: D.DkvKv8Score(**{**dict(softcap=0.0, window=0), **kw})  # noqa: E731
-    for bad in (dict(softcap=-1.0), dict(softcap=math.nan), dict(softcap=math.inf), dict(window=-1)):
+    for bad in (dict(softcap=-1.0), dict(softcap=math.nan), dict(softcap=math.inf), dict(softcap=1e-7),
+                dict(softcap=1e31), dict(window=-1)):
         assert attend(lib, score=score(**bad)) == ARG, bad
     assert attend(lib, cache=(256, 256, 1 << 30)) == UNS
     assert attend(lib, seqs=1 << 20, total=1 << 29, max_q=1 << 10) == UNS
