@@ -13,12 +13,13 @@
 //   warp 12         issues the MMAs (first CTA);  warp 13 looks up block ids and scales, four key tiles at a time
 //   warps 14, 15    of the second CTA pass on that its K or V is in place: a release at cluster scope takes about 1000
 //                   clocks, too long for the converters
-// The softmax warps take registers from the others (184 against 96 and 48), so that a thread holds its row's 128 scores.  P is
-// written over the columns of S that it came from.  While one row tile is in its softmax the tensor cores work for the
-// other; the chain S, softmax, P V of a row tile, about 5000 clocks a key tile, is what a key tile takes (the MMAs need
-// 2048 of them, exp2 as many).  Measured on 2048 queries at 32768 keys, 1.16 ms here: two warps a row 1.24 ms; 64-key
-// tiles with two S buffers, so that S never waits, 1.32 ms with two warps a row and 1.36 to 1.42 ms with one (more
-// hand-overs for each key); the row tiles taking turns at exp2 1.43 ms.
+// P is written over the columns of S that it came from.  The softmax goes through a tile's scores twice in tensor memory, 32
+// at a time by loops, and masks and caps are a loop too: with unrolled code the warps' different programs evict each other
+// from the instruction caches (the same source took 1.17 to 1.36 ms from build to build, 1.24 ms as it is).  While one
+// row tile is in its softmax the tensor cores work for the other; the chain S, softmax, P V of a row tile, about 5000 clocks
+// a key tile, is what a key tile takes (the MMAs need 2048 of them, exp2 as many).  Measured on 2048 queries at 32768
+// keys beside this: two warps a row 1.24 ms; 64-key tiles with two S buffers, so that S never waits, 1.32 ms with two
+// warps a row and 1.36 to 1.42 ms with one (more hand-overs for each key); the row tiles taking turns at exp2 1.43 ms.
 //
 // Codes are exact in fp16; scales stay out of the operands as in kv8_stream.cuh: the K scale multiplies the fp32 score,
 // the V scale is part of the exponent z = score + log2(v scale), and the sum of weights takes it out again.  The running
@@ -118,11 +119,6 @@ __device__ __forceinline__ void tmem_st_32x32b_x16(uint32_t taddr, const uint32_
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-// Register shares of the warpgroups; all warps of one execute it together.
-template <int N>
-__device__ __forceinline__ void regs_take() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void regs_give() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t r;
@@ -316,33 +312,30 @@ struct TileSoftmax {
       const bool whole = __all_sync(~0u, row.lo <= M.key0[0] && M.last <= row.hi);
       // raw: without a bias z is one fused multiply-add of the raw score, done again in the second pass.  m then is not
       // the exact maximum of those sums, but within a rounding of it, so scores whose rounding is not small against 1 take
-      // the other path: z made cell by cell in tensor memory, by a loop (unrolled code for all of them evicted the warps'
-      // other programs from the instruction caches).
-      uint32_t r[4][32];
+      // the other path: z made cell by cell in tensor memory.
       bool raw = !BIAS && whole;
       float top = -INFINITY;
       if (raw) {
+#pragma unroll 1
+        for (int c = 0; c < 4; ++c) {
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(s_tmem + 32 * c, r);
+          const float2 ks = reinterpret_cast<const float2*>(M.ks)[c], lv = reinterpret_cast<const float2*>(M.lv)[c];
+          tmem_ld_wait();
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(s_tmem + 32 * c, r[c]);
-        tmem_ld_wait();
+          for (int e = 0; e < 2; ++e) {
+            float y[4];
 #pragma unroll
-        for (int cell = 0; cell < kTileCells; ++cell) {
-          const uint32_t* x = &r[cell / 2][16 * (cell % 2)];
-          float y[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            y[i] = fmaxf(fmaxf(__uint_as_float(x[4 * i]), __uint_as_float(x[4 * i + 1])),
-                         fmaxf(__uint_as_float(x[4 * i + 2]), __uint_as_float(x[4 * i + 3])));
-          top = fmaxf(top, fmaf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), M.ks[cell] * scl2, M.lv[cell]));
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t* x = &r[16 * e + 4 * i];
+              y[i] = fmaxf(fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1])), fmaxf(__uint_as_float(x[2]), __uint_as_float(x[3])));
+            }
+            top = fmaxf(top, fmaf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])), (e ? ks.y : ks.x) * scl2, e ? lv.y : lv.x));
+          }
         }
         raw = __all_sync(~0u, fabsf(top) < 65536.0f);
       }
-      if (!raw) {
-        top = transform(M, whole, behind, two_over_cap, per_cap);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(s_tmem + 32 * c, r[c]);
-        tmem_ld_wait();
-      }
+      if (!raw) top = transform(M, whole, behind, two_over_cap, per_cap);
       const bool rise = top > m + kTileSlack;
       if (__any_sync(~0u, rise)) {
         const float now = rise ? top : m, fix = fast_exp2(m - now);
@@ -360,29 +353,32 @@ struct TileSoftmax {
           }
         }
       }
-#pragma unroll
+#pragma unroll 1
       for (int c = 0; c < 4; ++c) {
-        uint32_t p[16];
+        uint32_t r[32], p[16];
+        tmem_ld_32x32b_x32(s_tmem + 32 * c, r);
+        const float2 ks = reinterpret_cast<const float2*>(M.ks)[c], lv = reinterpret_cast<const float2*>(M.lv)[c];
+        const float2 iv = reinterpret_cast<const float2*>(M.iv)[c];
+        tmem_ld_wait();
 #pragma unroll
-        for (int gq = 0; gq < 2; ++gq) {
-          const int cell = 2 * c + gq;
-          const float kk = raw ? M.ks[cell] * scl2 : 1.0f, add = raw ? M.lv[cell] - m : -m;
+        for (int e = 0; e < 2; ++e) {
+          const float kk = raw ? (e ? ks.y : ks.x) * scl2 : 1.0f, add = raw ? (e ? lv.y : lv.x) - m : -m;
           const uint64_t kk2 = pack2(kk, kk), add_2 = pack2(add, add);
           uint64_t sum2 = 0;
+          float x, y;
 #pragma unroll
           for (int i = 0; i < 16; i += 2) {
-            float x, y;
-            unpack2(fma2(pack2(__uint_as_float(r[c][gq * 16 + i]), __uint_as_float(r[c][gq * 16 + i + 1])), kk2, add_2), x, y);
+            const uint32_t* q = &r[16 * e + i];
+            unpack2(fma2(pack2(__uint_as_float(q[0]), __uint_as_float(q[1])), kk2, add_2), x, y);
             x = fast_exp2(x), y = fast_exp2(y);
             sum2 = add2(sum2, pack2(x, y));
-            p[gq * 8 + i / 2] = pack_f16(x, y);
+            p[8 * e + i / 2] = pack_f16(x, y);
           }
-          float x, y;
           unpack2(sum2, x, y);
           x += y;
-          if (x != 0.f) l = fmaf(x, M.iv[cell], l);  // a cell out of sight adds nothing, even where its scale is NaN
+          if (x != 0.f) l = fmaf(x, e ? iv.y : iv.x, l);  // a cell out of sight adds nothing, even where its scale is NaN
         }
-        tmem_st_32x32b_x16(s_tmem + 16 * c, p);
+        tmem_st_32x32b_x16(s_tmem + 16 * c, p);  // over scores that this thread has read
       }
       tmem_st_wait();
       tc_fence_before();
@@ -632,9 +628,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
     }
   };
 
-  // per sub-partition: 2 x 184 + 96 + 48 = 4 x 128 registers a thread, what the CTA was launched with
   if (warp < 8) {
-    regs_take<184>();
     const int tile = warp / 4;
     if (tile < tiles) {
       const uint32_t lanes = static_cast<uint32_t>(warp % 4) << 21;  // (32 * quarter) << 16
@@ -691,10 +685,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTileThreads, 1)
       tc_fence_before();
     }
   } else if (warp < 12) {
-    regs_give<96>();
     convert();
   } else {
-    regs_give<48>();
     if (warp == 12 && rank == 0 && n > 0) issue_mmas();
     if (warp >= 14 && lane == 0 && rank == 1) pass_on(warp == 14 ? bars.k_full : bars.v_full);
     __syncwarp();
