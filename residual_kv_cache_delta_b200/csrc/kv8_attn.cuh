@@ -6,8 +6,16 @@
 
 namespace dkv {
 
-// Up to so many rows per kv head the streaming kernel is taken, above it the tcgen05 one.
-constexpr int kStreamMaxRows = 16;
+// Up to so many rows per kv head the streaming kernel is taken (in row tiles of 16), above it the tcgen05 one, whose time
+// hardly depends on the rows below its tile.  Microseconds of the first and the second, 8 kv heads, int8:
+//                      16 rows         32 rows         64 rows
+//   d 128,  8 x  5000   30.6 and  94.8  48.8 and  94.9  94.6 and  96.7
+//           8 x 32768    154 and   541   284 and   537   513 and   539
+//           1 x  2000   11.4 and  16.5  11.8 and  16.8  13.9 and  17.8
+//   d  64,  8 x  5000   22.4 and  78.5  32.9 and  78.4  52.7 and  80.3
+//           8 x 32768   86.1 and   453   159 and   452   286 and   453
+// At d = 128 the two are close at 64 rows.  At d = 64 the streaming kernel still leads there; more rows were not measured.
+constexpr int kStreamMaxRows = 64;
 
 // How many query rows a CTA takes and how many key ranges a row is cut into.
 struct Kv8Plan {
@@ -47,7 +55,8 @@ int kv8_attn_splits(const dkv_kv8_shape& sh, int num_seqs, int max_q, int max_ct
 }
 
 // Joins the splits of each row; starts while the attention kernel's last CTAs run.  With more than 8 splits four warps share
-// a row.
+// a row: for one sequence of 131072 tokens, 64 rows, the join took 31 us with one warp a row and 8 us with four (both from a
+// profiler's launch list, caches cold).  With few splits one warp reads them in few steps, and a CTA of four rows serves.
 template <typename T, int D>
 static dkv_status launch_combine(const Kv8Attn& p, cudaStream_t st) {
   if (p.nsplit == 1) return DKV_OK;

@@ -1,4 +1,5 @@
-// Attention over the 8-bit cache on CUDA cores, fp32 arithmetic throughout.
+// Attention over the 8-bit cache on CUDA cores, fp32 arithmetic throughout: the path of fp32 tensors.  8 x 32768 tokens of
+// d = 128, 4 heads per kv head took it 864 us with bf16 tensors, 0.6 TB/s: memory does not bound it.
 //
 // One CTA takes kRows query rows (a row is a query token and a head of the kv head's group) and a range of keys.
 // Tiles of 32 keys are dequantised into shared memory; a warp scores two rows against the tile (one key per lane),
