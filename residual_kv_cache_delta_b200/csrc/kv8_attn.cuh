@@ -9,11 +9,13 @@ namespace dkv {
 // Up to so many rows per kv head the streaming kernel is taken (in row tiles of 16), above it the tcgen05 one, whose time
 // hardly depends on the rows below its tile.  Microseconds of the first and the second, 8 kv heads, int8:
 //                      16 rows         32 rows         64 rows
-//   d 128,  8 x  5000   30.6 and  94.8  48.8 and  94.9  94.6 and  96.7
-//           8 x 32768    154 and   541   284 and   537   513 and   539
-//           1 x  2000   11.4 and  16.5  11.8 and  16.8  13.9 and  17.8
-//   d  64,  8 x  5000   22.4 and  78.5  32.9 and  78.4  52.7 and  80.3
-//           8 x 32768   86.1 and   453   159 and   452   286 and   453
+//   d 128,  8 x  5000   30.5 and  94.8  48.7 and  94.9  94.6 and  96.7
+//           8 x 32768    153 and   541   281 and   537   510 and   539
+//           1 x  2000   11.5 and  16.5  11.7 and  16.8  13.9 and  17.8
+//   d  64,  8 x  5000   22.9 and  78.5  34.2 and  78.4  56.2 and  80.3
+//           8 x 32768   90.7 and   453   169 and   452   307 and   453
+//           1 x  2000   10.9 and  15.0  11.2 and  15.8  13.3 and  16.2
+// (The second figures are of builds with a lower limit, whose code is laid out differently: some per cent either way.)
 // At d = 128 the two are close at 64 rows.  At d = 64 the streaming kernel still leads there; more rows were not measured.
 constexpr int kStreamMaxRows = 64;
 
