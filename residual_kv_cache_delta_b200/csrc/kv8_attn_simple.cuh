@@ -105,7 +105,7 @@ __global__ void __launch_bounds__(128) kv8_attn_simple_kernel(const Kv8Attn a, i
     const int key = span.cell(cell) * kKv8CellKeys + lane % kKv8CellKeys;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      float z = a.softcap > 0.f ? kv8_cap(d[j], a.softcap, 2.0f * kLog2e / a.softcap) : d[j];
+      float z = a.softcap > 0.f ? a.softcap * tanhf(d[j] / a.softcap) : d[j];
       z = z * kLog2e - slope[j] * abs(row[j].pos - key);
       if (!there || !kv8_sees(row[j], sq_.prefix, key)) z = -INFINITY;
       float top = z;

@@ -243,7 +243,9 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas<D>(NT))
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[c][i][j] = 0.f;
   }
-  const float two_over_cap = BIAS && a.softcap > 0.f ? 2.0f * kLog2e / a.softcap : 0.f;
+  // z = tanh(s into) out_of, or s into without a cap, s the score in natural units
+  const bool cap = BIAS && a.softcap > 0.f;
+  const float into = cap ? 1.0f / a.softcap : kLog2e, out_of = a.softcap * kLog2e;
   const int kg = stream_perm<D>(g);
   int kt[4];  // keys whose V a lane reads
 #pragma unroll
@@ -298,24 +300,32 @@ __global__ void __launch_bounds__(kStreamWarps * 32, stream_ctas<D>(NT))
       for (int c = 0; c < NT; ++c) {
         float z[4];
         bool over = false;
-        const float kk[2] = {ks * scl[c][0], ks * scl[c][1]};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          z[i] = sc[c][0][i] + sc[c][1][i];
-          if (!BIAS) z[i] = fmaf(z[i], kk[i & 1], lv);
-        }
+        float kk[2] = {ks * scl[c][0], ks * scl[c][1]};
+        if (BIAS) kk[0] *= into, kk[1] *= into;
+        float add[4] = {lv, lv, lv, lv};
         if (BIAS) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) z[i] *= kk[i & 1];
-          if (a.softcap > 0.f)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) z[i] = kv8_cap(z[i], a.softcap, two_over_cap);
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const float gap = static_cast<float>(row[c][e].pos - key0 - kg);
-            z[e] = fmaf(-slope[c][e], fabsf(gap), fmaf(z[e], kLog2e, lv));
-            z[2 + e] = fmaf(-slope[c][e], fabsf(gap - 8.f), fmaf(z[2 + e], kLog2e, lv));
+            add[e] = fmaf(-slope[c][e], fabsf(gap), lv), add[2 + e] = fmaf(-slope[c][e], fabsf(gap - 8.f), lv);
           }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[i] = sc[c][0][i] + sc[c][1][i];
+        if (cap) {
+          float most = 0.f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) z[i] *= kk[i & 1], most = fmaxf(most, z[i] * z[i]);
+          if (__all_sync(~0u, most <= kCapNear)) {  // the usual case, without special functions
+#pragma unroll
+            for (int i = 0; i < 4; ++i) z[i] = fmaf(kv8_tanh_near(z[i]), out_of, add[i]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) z[i] = fmaf(kv8_tanh(z[i]), out_of, add[i]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) z[i] = fmaf(z[i], kk[i & 1], add[i]);
         }
         if (!whole) {
 #pragma unroll

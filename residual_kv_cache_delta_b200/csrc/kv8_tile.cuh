@@ -221,28 +221,28 @@ struct TileSoftmax {
   float scl, slope;  // row scale times the softmax scale (natural units); slope in log2 units
   float m, l;
 
-  // The scores of cell `cell` (16 columns) as z, in place.
-  __device__ __forceinline__ void scores(const TileMeta& M, int cell, uint32_t (&r)[16], float two_over_cap) {
-    const float kk = M.ks[cell] * scl, lv = M.lv[cell], gap = static_cast<float>(row.pos - M.key0[cell]);
+  // The scores of cell `cell` (16 columns) as z, in place.  into, out_of: z = tanh(s into) out_of, or s into without a cap.
+  __device__ __forceinline__ void scores(const TileMeta& M, int cell, uint32_t (&r)[16], float into, float out_of) {
+    const float kk = M.ks[cell] * scl * into, lv = M.lv[cell], gap = static_cast<float>(row.pos - M.key0[cell]);
+    const bool cap = BIAS && a.softcap > 0.f;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-      float x = __uint_as_float(r[i]) * kk;
-      if (BIAS && a.softcap > 0.f) x = kv8_cap(x, a.softcap, two_over_cap);
-      x = fmaf(x, kLog2e, lv);
+      float x = __uint_as_float(r[i]);
+      x = cap ? fmaf(kv8_tanh(x * kk), out_of, lv) : fmaf(x, kk, lv);
       if (BIAS) x = fmaf(-slope, fabsf(gap - static_cast<float>(i)), x);
       r[i] = __float_as_uint(x);
     }
   }
 
   // The same without masks, for keys that stand at or before the row's position (or no distance bias), two columns to an
-  // instruction.  Capped scores: tanh(y) = y P(y^2) with a polynomial (Chebyshev interpolation of degree 4 in y^2 on [0,
-  // 0.36], relative error 7.2e-8), where exp2 and a reciprocal would keep the special-function unit for three times as long
-  // as the softmax's own exp2 does; `most` is raised to the largest y^2, which must stay within 0.36.
-  __device__ __forceinline__ void scores_quick(const TileMeta& M, int cell, uint32_t (&r)[16], float per_cap, float& most) {
+  // instruction.  Capped scores: by kv8_tanh_near alone, where exp2 and a reciprocal would keep the special-function unit for
+  // three times as long as the softmax's own exp2 does; `most` is raised to the largest y^2, which must stay within kCapNear.
+  __device__ __forceinline__ void scores_quick(const TileMeta& M, int cell, uint32_t (&r)[16], float into, float out_of,
+                                               float& most) {
     const float lv = fmaf(-slope, static_cast<float>(row.pos - M.key0[cell]), M.lv[cell]);
     const bool cap = a.softcap > 0.f;
-    const float kk = M.ks[cell] * scl * (cap ? per_cap : kLog2e), out = a.softcap * kLog2e;
-    const uint64_t kk2 = pack2(kk, kk), out2 = pack2(out, out), lv2 = pack2(lv, lv), sl2 = pack2(slope, slope);
+    const float kk = M.ks[cell] * scl * into;
+    const uint64_t kk2 = pack2(kk, kk), out2 = pack2(out_of, out_of), lv2 = pack2(lv, lv), sl2 = pack2(slope, slope);
 #pragma unroll
     for (int i = 0; i < 16; i += 2) {
       uint64_t y = mul2(pack2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), kk2);
@@ -251,10 +251,10 @@ struct TileSoftmax {
         const uint64_t u = mul2(y, y);
         unpack2(u, x0, x1);
         most = fmaxf(fmaxf(most, x0), x1);
-        uint64_t p = fma2(u, pack2(0.01548669021576643f, 0.01548669021576643f), pack2(-0.052109625190496445f, -0.052109625190496445f));
-        p = fma2(u, p, pack2(0.13310357928276062f, 0.13310357928276062f));
-        p = fma2(u, p, pack2(-0.33332324028015137f, -0.33332324028015137f));
-        p = fma2(u, p, pack2(0.9999999403953552f, 0.9999999403953552f));
+        uint64_t p = fma2(u, pack2(kCapP4, kCapP4), pack2(kCapP3, kCapP3));
+        p = fma2(u, p, pack2(kCapP2, kCapP2));
+        p = fma2(u, p, pack2(kCapP1, kCapP1));
+        p = fma2(u, p, pack2(kCapP0, kCapP0));
         y = mul2(mul2(y, p), out2);
       }
       y = add2(y, fma2(sl2, pack2(static_cast<float>(i), static_cast<float>(i + 1)), lv2));
@@ -264,7 +264,7 @@ struct TileSoftmax {
   }
 
   // The row's scores in tensor memory as z, masked unless `whole`; returns their maximum.
-  __device__ __forceinline__ float transform(const TileMeta& M, bool whole, bool behind, float two_over_cap, float per_cap) {
+  __device__ __forceinline__ float transform(const TileMeta& M, bool whole, bool behind, float into, float out_of) {
     float top = -INFINITY;
 #pragma unroll 1
     for (int cell = 0; cell < kTileCells; ++cell) {
@@ -274,14 +274,14 @@ struct TileSoftmax {
       bool quick = BIAS && behind;
       if (quick) {
         float most = 0.f;
-        scores_quick(M, cell, r, per_cap, most);
-        quick = __all_sync(~0u, most <= 0.36f);
+        scores_quick(M, cell, r, into, out_of, most);
+        quick = __all_sync(~0u, most <= kCapNear);
         if (!quick) {
           tmem_ld_32x32b_x16(s_tmem + 16 * cell, r);
           tmem_ld_wait();
         }
       }
-      if (!quick) scores(M, cell, r, two_over_cap);
+      if (!quick) scores(M, cell, r, into, out_of);
       if (!whole) {
         const uint32_t bits = (M.there >> cell) & 1 ? cell_bits(row, seq.prefix, M.key0[cell]) : 0u;
 #pragma unroll
@@ -298,9 +298,8 @@ struct TileSoftmax {
 
   __device__ __forceinline__ bool run(int n) {
     const float scl2 = scl * kLog2e;
-    const float per_cap = BIAS && a.softcap > 0.f ? 1.0f / a.softcap : 0.f;
+    const float into = BIAS && a.softcap > 0.f ? 1.0f / a.softcap : kLog2e, out_of = a.softcap * kLog2e;
     const bool behind = BIAS && __all_sync(~0u, slope == 0.f || seq.prefix <= row.pos + 1);
-    const float two_over_cap = BIAS && a.softcap > 0.f ? 2.0f * kLog2e / a.softcap : 0.f;
     for (int j = 0; j < n; ++j) {
       bool ok = true;
       if (j % kMetaBatch == 0)
@@ -335,7 +334,7 @@ struct TileSoftmax {
         }
         raw = __all_sync(~0u, fabsf(top) < 65536.0f);
       }
-      if (!raw) top = transform(M, whole, behind, two_over_cap, per_cap);
+      if (!raw) top = transform(M, whole, behind, into, out_of);
       const bool rise = top > m + kTileSlack;
       if (__any_sync(~0u, rise)) {
         const float now = rise ? top : m, fix = fast_exp2(m - now);
