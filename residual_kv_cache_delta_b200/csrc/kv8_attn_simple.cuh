@@ -3,7 +3,9 @@
 //
 // One CTA takes kRows query rows (a row is a query token and a head of the kv head's group) and a range of keys.
 // Tiles of 32 keys are dequantised into shared memory; a warp scores two rows against the tile (one key per lane),
-// updates their running maximum and sum, and the CTA's threads, one per output dimension, add p * V.
+// updates their running maximum and sum, and the CTA's threads, one per output dimension, add p * V.  V lies there as codes and
+// its scale is part of the row's weight, which is 0 for a key out of the row's sight: a block whose scale is NaN then
+// reaches only the rows that see it.
 #pragma once
 
 #include "kv8_common.cuh"
@@ -20,6 +22,7 @@ __global__ void __launch_bounds__(128) kv8_attn_simple_kernel(const Kv8Attn a, i
   __shared__ __align__(16) float sq[kSimpleRows * D];
   __shared__ float sp[kSimpleRows][kSimpleKeys];
   __shared__ float sfix[kSimpleRows];
+  __shared__ float svs[kSimpleKeys];   // V scale of the tile's key
   __shared__ int sthere[kSimpleKeys];  // whether the tile's key lies in the context, in a mapped block
   __shared__ float sm[kSimpleRows], sl[kSimpleRows];
   griddep_launch_dependents();
@@ -64,7 +67,7 @@ __global__ void __launch_bounds__(128) kv8_attn_simple_kernel(const Kv8Attn a, i
     for (int e = tid; e < kSimpleKeys * D / 16; e += 128) {  // 16 codes of K and of V
       const int k = e / (D / 16), c = (e % (D / 16)) * 16;
       const int cell = v + k / kKv8CellKeys;
-      float kf[16] = {}, vf[16] = {};
+      float kf[16] = {}, vf[16] = {}, vs = 0.f;
       int there = 0;
       if (cell < v1) {
         const int key = span.cell(cell) * kKv8CellKeys + k % kKv8CellKeys;
@@ -76,18 +79,19 @@ __global__ void __launch_bounds__(128) kv8_attn_simple_kernel(const Kv8Attn a, i
           const uint4 kw = *reinterpret_cast<const uint4*>(src);
           const uint4 vw = *reinterpret_cast<const uint4*>(src + static_cast<int64_t>(a.block) * D);
           there = 1;
-          const float ks = a.scales[cellbase], vs = a.scales[cellbase + 1];
+          const float ks = a.scales[cellbase];
+          vs = a.scales[cellbase + 1];
           const uint32_t kk[4] = {kw.x, kw.y, kw.z, kw.w}, vv[4] = {vw.x, vw.y, vw.z, vw.w};
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             kf[j] = kv8_decode<E4M3>(static_cast<uint8_t>(kk[j / 4] >> (8 * (j % 4)))) * ks;
-            vf[j] = kv8_decode<E4M3>(static_cast<uint8_t>(vv[j / 4] >> (8 * (j % 4)))) * vs;
+            vf[j] = kv8_decode<E4M3>(static_cast<uint8_t>(vv[j / 4] >> (8 * (j % 4))));
           }
         }
       }
 #pragma unroll
       for (int j = 0; j < 16; ++j) sk[k * kPad + c + j] = kf[j], sv[k * D + c + j] = vf[j];
-      if (c == 0) sthere[k] = there;
+      if (c == 0) sthere[k] = there, svs[k] = vs;
     }
     __syncthreads();
     const bool there = sthere[lane] != 0;
@@ -107,7 +111,8 @@ __global__ void __launch_bounds__(128) kv8_attn_simple_kernel(const Kv8Attn a, i
     for (int j = 0; j < 2; ++j) {
       float z = a.softcap > 0.f ? a.softcap * tanhf(d[j] / a.softcap) : d[j];
       z = z * kLog2e - slope[j] * abs(row[j].pos - key);
-      if (!there || !kv8_sees(row[j], sq_.prefix, key)) z = -INFINITY;
+      const bool seen = there && kv8_sees(row[j], sq_.prefix, key);
+      if (!seen) z = -INFINITY;
       float top = z;
 #pragma unroll
       for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(~0u, top, o));
@@ -115,7 +120,7 @@ __global__ void __launch_bounds__(128) kv8_attn_simple_kernel(const Kv8Attn a, i
       const float p = exp2f(z - top), fix = exp2f(m[j] - top);
       m[j] = top;
       l[j] = l[j] * fix + p;
-      sp[warp * 2 + j][lane] = p;
+      sp[warp * 2 + j][lane] = seen ? p * svs[lane] : 0.f;
       if (lane == 0) sfix[warp * 2 + j] = fix;
     }
     __syncthreads();

@@ -647,3 +647,30 @@ def test_compressed_past_and_8_bit_recent_tokens_merge_into_one_attention():
         assert ((got - want).abs() <= want_err).all()
         assert (got - want).norm() <= (1e-2 + 2.0 ** -8) * want.norm()
         assert (l[s].double().cpu() - want_l).abs().max() <= 1e-3
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+@pytest.mark.parametrize("code", ["int8", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_poisoned_v_blocks_reach_only_the_rows_that_see_them(dtype, code, d):
+    """A block whose V scale is NaN, in front of some rows of a CTA and behind or outside the others' sight: causal rows of one
+    sequence, windows, packed documents, a prefix."""
+    shape = D.KV8Shape(2, 1, d, 16, dtype, code)
+    g = _gen(47)
+    for nq, T, block in ((4, 66, 4), (40, 90, 4), (60, 200, 8)):
+        codes, scales, table = K.cache_for(shape, [T], g)
+        q = torch.randn(nq, 2, d, generator=g).to(dtype)
+        p = T - nq + torch.arange(nq)
+        bad = scales.clone()
+        bad[table[0, block].long(), 0, 1] = math.nan
+        first = torch.where(p % 2 == 0, 0, 16 * block + 16).to(torch.int32)
+        for kw in (dict(), dict(window=20), dict(first=first), dict(window=5, prefix=torch.tensor([40], dtype=torch.int32))):
+            out, lse = K.run_attention(shape, codes, bad, table, q, [0, nq], [T], "cuda", **kw)
+            ro, rl, to, tl = K.attention(shape, codes, scales, table, q, [0, nq], [T], **kw)
+            see = K.visible(nq, T, kw.get("window", 0), int(kw["prefix"][0]) if "prefix" in kw else 0,
+                            first.long() if "first" in kw else None)
+            hit = see[:, 16 * block:16 * block + 16].any(1)
+            assert hit.any() and not hit.all() or nq == 60 and not kw
+            assert out[hit].isnan().all()
+            K.check(out[~hit], ro[~hit], to[~hit], "out")
+            K.check(lse[~hit], rl[~hit], tl[~hit], "lse")
