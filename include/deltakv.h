@@ -395,7 +395,8 @@ dkv_status deltakv_kv8_cache_bytes(const dkv_kv8_shape* shape, int32_t num_block
  *   q, q_out      NULL, or queries of the same tokens to be rotated by the same angles: q strided like k_new (H_q
  *                 heads), q_out [total_new][H_q][d]; needs `rope`.  q_out may be q (same address, stride H_q * d)
  * Writes the new tokens' codes, their blocks' scales (and re-coded earlier rows of a block whose scale grew) and
- * q_out; all else stays as it was.
+ * q_out; all else stays as it was.  A sequence whose lengths break a bound (more than max_new tokens, rows behind
+ * total_new, a negative start) is recorded (DKV_DEVERR_BOUNDS) and nothing of it is written, q_out included.
  */
 dkv_status deltakv_kv8_append(const dkv_kv8_shape* shape, const dkv_kv8_cache* cache, const dkv_kv8_rope* rope,
                               const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,

@@ -39,6 +39,19 @@ struct Kv8Append {
   float neg_zero;      // -0, not known to the compiler
 };
 
+// Rows of one sequence of an append; ok = false when they break a bound (nothing of the sequence is written then).
+struct AppendSeq {
+  int row0, n, start;
+  bool ok;
+};
+__device__ __forceinline__ AppendSeq append_seq(const Kv8Append& a, int s) {
+  AppendSeq v;
+  v.row0 = a.cu_new[s], v.n = a.cu_new[s + 1] - v.row0, v.start = a.start_pos[s];
+  v.ok = v.row0 >= 0 && v.n <= a.max_new && static_cast<int64_t>(v.row0) + v.n <= a.total_new && v.start >= 0 &&
+         static_cast<int64_t>(v.start) + v.n <= INT32_MAX - 64;  // positions of a block's rows fit an int
+  return v;
+}
+
 // Eight values of type T as they lie in memory.
 template <typename T>
 struct Oct;
@@ -210,8 +223,10 @@ __device__ __forceinline__ void append_q(const Kv8Append& a, int64_t cta) {
     const int mid = (lo + hi) >> 1;
     if (a.cu_new[mid] <= tok) lo = mid; else hi = mid;
   }
-  if (tok < a.cu_new[lo] || tok >= a.cu_new[lo + 1]) return;  // a row of no sequence
-  const int pos = a.positions ? a.positions[tok] : a.start_pos[lo] + static_cast<int>(tok - a.cu_new[lo]);
+  const AppendSeq q = append_seq(a, lo);
+  // a row of no sequence, or of one that the K and V part records and refuses
+  if (tok < q.row0 || tok >= static_cast<int64_t>(q.row0) + q.n || !q.ok) return;
+  const int pos = a.positions ? a.positions[tok] : q.start + static_cast<int>(tok - q.row0);
   float cs[16], x[16];
   const uint64_t nz = pack2(a.neg_zero, a.neg_zero);
   const bool turn = load_angles(a, pos, u, cs);
@@ -245,10 +260,10 @@ __global__ void __maxnreg__(80) kv8_append_kernel(const __grid_constant__ Kv8App
   const int h0 = static_cast<int>(id % steps) * kN, h1 = min(h0 + kN, a.heads);
   id /= steps;
   const int nth = static_cast<int>(id % a.blocks_per_seq), s = static_cast<int>(id / a.blocks_per_seq);
-  const int row0 = a.cu_new[s], n = a.cu_new[s + 1] - row0, start = a.start_pos[s];
+  const AppendSeq seq = append_seq(a, s);
+  const int row0 = seq.row0, n = seq.n, start = seq.start;
   if (n <= 0) return;
-  if (row0 < 0 || n > a.max_new || static_cast<int64_t>(row0) + n > a.total_new || start < 0 ||
-      start > INT32_MAX - 64 - n) {  // positions of a block's rows fit an int
+  if (!seq.ok) {
     if (threadIdx.x == 0) record_error(DKV_DEVERR_BOUNDS);
     return;
   }

@@ -674,3 +674,32 @@ def test_poisoned_v_blocks_reach_only_the_rows_that_see_them(dtype, code, d):
             assert out[hit].isnan().all()
             K.check(out[~hit], ro[~hit], to[~hit], "out")
             K.check(lse[~hit], rl[~hit], tl[~hit], "lse")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_append_leaves_the_queries_of_refused_sequences(dtype):
+    """A sequence whose lengths break a bound is recorded and nothing of it is written: not its queries either, in place or
+    not; the other sequence's are rotated."""
+    shape = D.KV8Shape(4, 1, 64, 16, dtype, "int8")
+    g = _gen(53)
+    codes, scales, table = K.cache_for(shape, [40, 40], g)
+    k = torch.randn(20, 1, 64, generator=g).to(dtype)
+    q = torch.randn(20, 4, 64, generator=g).to(dtype)
+    rope = _rope(64, 64, g)
+    for cu, start, bad in (([0, 10, 20], [3, -1], 1), ([0, 12, 20], [0, 5], 0), ([0, 10, 25], [7, 0], 1),
+                           ([0, 10, 20], [0, (1 << 31) - 20], 1)):
+        for inplace in (False, True):
+            cache = D.KV8Cache(codes.cuda(), scales.cuda())
+            dq = q.cuda()
+            q_out = dq if inplace else torch.full_like(dq, 7.0)
+            D.deltakv_kv8_append(shape, cache, k.cuda(), k.cuda(), _i32(cu), _i32(start), table.cuda(), 10,
+                                 rope=rope.cuda(), q=dq, q_out=q_out)
+            assert D.deltakv_get_device_error() == 3
+            got = q_out.cpu()
+            for s in (0, 1):
+                rows = slice(cu[s], min(cu[s + 1], 20))
+                if s == bad:
+                    want = q[rows] if inplace else torch.full_like(q[rows], 7.0)
+                else:
+                    want = K.rotate(q[rows], rope[start[s]:start[s] + cu[s + 1] - cu[s]], False).to(dtype)
+                assert torch.equal(got[rows], want), (cu, start, inplace, s)
