@@ -475,8 +475,8 @@ dkv_status deltakv_kv8_append(const dkv_kv8_shape* shape, const dkv_kv8_cache* c
                           rope->max_pos <= 0 || rope->table == nullptr || !aligned16(rope->table)))
     return DKV_ERR_INVALID_ARG;
   if ((q == nullptr) != (q_out == nullptr) || (q != nullptr && rope == nullptr)) return DKV_ERR_INVALID_ARG;
-  if (num_seqs == 0 || total_new == 0 || max_new == 0) return DKV_OK;
-  if (total_new > static_cast<int64_t>(num_seqs) * max_new) return DKV_ERR_INVALID_ARG;
+  if (total_new > static_cast<int64_t>(num_seqs) * max_new) return DKV_ERR_INVALID_ARG;  // tokens, but no room for them
+  if (total_new == 0) return DKV_OK;
   if (total_new > INT32_MAX) return DKV_ERR_UNSUPPORTED;
   if (k_new == nullptr || v_new == nullptr || cu_new == nullptr || start_pos == nullptr || block_tables == nullptr)
     return DKV_ERR_INVALID_ARG;

@@ -160,3 +160,13 @@ def test_binding_refuses_tensors_that_do_not_fit(lib):
         D.deltakv_merge_attention([q] * 9, [q[..., 0].float()] * 9, q, None)
     with pytest.raises(ValueError):
         D.deltakv_merge_attention([q.half()], [q[..., 0].float()], q.half(), None)
+
+
+def test_append_refuses_tokens_without_room_for_them(lib):
+    """New tokens, but no sequence or a bound of 0 per sequence: refused as attention refuses it, not passed over."""
+    for bad in (dict(max_new=0), dict(seqs=0), dict(seqs=0, max_new=0), dict(total=1, max_new=0)):
+        assert append(lib, **bad) == ARG, bad
+    for bad in (dict(max_q=0), dict(seqs=0)):
+        assert attend(lib, **bad) == ARG, bad
+    for nothing in (dict(total=0, max_new=0, seqs=0), dict(total=0), dict(total=0, k=0, v=0, cu=0)):
+        assert append(lib, **nothing) == OK, nothing
