@@ -404,7 +404,8 @@ dkv_status deltakv_kv8_append(const dkv_kv8_shape* shape, const dkv_kv8_cache* c
                               int32_t max_blocks, int32_t num_seqs, int64_t total_new, int32_t max_new, const void* q,
                               int64_t q_stride, void* q_out, void* stream);
 
-/* Workspace needed by deltakv_kv8_attention for these host-side bounds (host output `bytes`). */
+/* Workspace needed by deltakv_kv8_attention for these host-side bounds (host output `bytes`).  The size never falls as a bound
+ * grows: a workspace for a program's largest batch, step and context serves all its smaller calls too. */
 dkv_status deltakv_kv8_attention_workspace(const dkv_kv8_shape* shape, int32_t num_seqs, int64_t total_q,
                                            int32_t max_q, int32_t max_ctx, size_t* bytes);
 
@@ -424,7 +425,7 @@ dkv_status deltakv_kv8_attention_workspace(const dkv_kv8_shape* shape, int32_t n
  *   softmax_scale <= 0 selects 1/sqrt(d)
  *   out           [total_q][H_q][d] dtype;  lse [total_q][H_q] float32 or NULL.  Rows of no sequence stay as they were
  *   workspace     >= deltakv_kv8_attention_workspace(shape, num_seqs, total_q, max_q, max_ctx) bytes, 256-byte
- *                 aligned; NULL when that is 0
+ *                 aligned; NULL when that is 0.  Its contents need not be kept between calls
  * A sequence whose lengths break a bound is recorded (DKV_DEVERR_BOUNDS) and its rows are left as they were.
  */
 dkv_status deltakv_kv8_attention(const dkv_kv8_shape* shape, const dkv_kv8_cache* cache, const dkv_kv8_score* score,

@@ -499,7 +499,7 @@ dkv_status deltakv_kv8_attention_workspace(const dkv_kv8_shape* s, int32_t num_s
   if (st != DKV_OK) return st;
   if (bytes == nullptr) return DKV_ERR_INVALID_ARG;
   if ((st = check_kv8_bounds(s, num_seqs, total_q, max_q, max_ctx)) != DKV_OK) return st;
-  *bytes = dkv::kv8_attn_layout(*s, dkv::kv8_attn_splits(*s, num_seqs, max_q, max_ctx), total_q).total;
+  *bytes = dkv::kv8_attn_layout(*s, dkv::kv8_attn_staged(*s, total_q, max_q, max_ctx)).total;
   return DKV_OK;
 }
 
@@ -522,15 +522,15 @@ dkv_status deltakv_kv8_attention(const dkv_kv8_shape* shape, const dkv_kv8_cache
   if (q == nullptr || context_lens == nullptr || block_tables == nullptr || out == nullptr) return DKV_ERR_INVALID_ARG;
   if (!kv8_rows_ok(shape, q, q_stride, shape->num_q_heads) || !aligned16(out)) return DKV_ERR_INVALID_ARG;
   if ((st = check_kv8_cache(shape, cache)) != DKV_OK) return st;
-  const dkv::Kv8AttnWs w =
-      dkv::kv8_attn_layout(*shape, dkv::kv8_attn_splits(*shape, num_seqs, max_q, max_ctx), total_q);
-  if (w.total > 0) {
+  const dkv::Kv8AttnWs w = dkv::kv8_attn_layout(*shape, dkv::kv8_attn_staged(*shape, total_q, max_q, max_ctx));
+  const int nsplit = dkv::kv8_attn_splits(*shape, num_seqs, max_q, max_ctx);
+  if (nsplit > 1) {  // otherwise the workspace is not touched
     if (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 256 != 0) return DKV_ERR_INVALID_ARG;
     if (workspace_bytes < w.total) return DKV_ERR_WORKSPACE;
   }
   dkv::Kv8AttnArgs a{shape,    cache,   score, q,       q_stride,      cu_q, context_lens, block_tables, max_blocks,
                      num_seqs, total_q, max_q, max_ctx, softmax_scale, out,  lse};
-  return dkv::launch_kv8_attention(a, w, workspace, static_cast<cudaStream_t>(stream));
+  return dkv::launch_kv8_attention(a, nsplit, w, workspace, static_cast<cudaStream_t>(stream));
 }
 
 dkv_status deltakv_merge_attention(int32_t dtype, int32_t head_dim, int64_t num_rows, int32_t num_parts,

@@ -1,5 +1,5 @@
 // Host-side arguments, launch choices and workspace layout of the 8-bit paged cache (deltakv_kv8_*) and of
-// deltakv_merge_attention.  The workspace query and the attention call both derive the split plan from here.
+// deltakv_merge_attention.  The workspace query and the attention call both derive the layout from here.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -55,15 +55,13 @@ struct Kv8AttnArgs {
 // Workspace of an attention call: per split and query row the running maximum and sum (log2 domain) and the
 // unnormalised output row, all fp32.  One split: nothing is staged.
 struct Kv8AttnWs {
-  int nsplit = 1;
   size_t ml = 0, o = 0, total = 0;
 };
 
-inline Kv8AttnWs kv8_attn_layout(const dkv_kv8_shape& sh, int nsplit, int64_t total_q) {
+inline Kv8AttnWs kv8_attn_layout(const dkv_kv8_shape& sh, int64_t staged_rows) {
   Kv8AttnWs w;
-  w.nsplit = nsplit;
-  if (nsplit > 1) {
-    const size_t rows = static_cast<size_t>(nsplit) * total_q * sh.num_q_heads;
+  if (staged_rows > 0) {
+    const size_t rows = static_cast<size_t>(staged_rows);
     w.o = align_up(rows * 8, kWsAlign);
     w.total = align_up(w.o + rows * sh.head_dim * 4, kWsAlign);
   }
@@ -71,8 +69,9 @@ inline Kv8AttnWs kv8_attn_layout(const dkv_kv8_shape& sh, int nsplit, int64_t to
 }
 
 dkv_status launch_kv8_append(const Kv8AppendArgs& a, cudaStream_t st);
-int kv8_attn_splits(const dkv_kv8_shape& sh, int num_seqs, int max_q, int max_ctx);
-dkv_status launch_kv8_attention(const Kv8AttnArgs& a, const Kv8AttnWs& w, void* workspace, cudaStream_t st);
+int kv8_attn_splits(const dkv_kv8_shape& sh, int num_seqs, int max_q, int span);
+int64_t kv8_attn_staged(const dkv_kv8_shape& sh, int64_t total_q, int max_q, int max_ctx);
+dkv_status launch_kv8_attention(const Kv8AttnArgs& a, int nsplit, const Kv8AttnWs& w, void* workspace, cudaStream_t st);
 dkv_status launch_merge(int dtype, int64_t rows, int head_dim, int n, const void* const* outs,
                         const float* const* lses, void* out, float* lse, cudaStream_t st);
 

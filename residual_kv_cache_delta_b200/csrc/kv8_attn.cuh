@@ -19,41 +19,64 @@ namespace dkv {
 // At d = 128 the two are close at 64 rows.  At d = 64 the streaming kernel still leads there; more rows were not measured.
 constexpr int kStreamMaxRows = 64;
 
-// How many query rows a CTA takes and how many key ranges a row is cut into.
-struct Kv8Plan {
-  int tile, nsplit;
+// The kernel of a call: how many query rows a CTA (tcgen05: a pair) takes, how many of them an SM holds, and the most CTAs
+// that a call with splits may have.  That limit bounds the workspace (most x tile staged rows).  It is 16 rounds of CTAs (12
+// of the tcgen05 kernel's, whose CTAs stage 512 rows): by the split plan's model, a call that it keeps from splitting loses a
+// tenth at most, at 524288 keys.
+struct Kv8Kind {
+  bool tiles;
+  int tile, per_sm;
+  int64_t slots, most;
 };
 
-// span: most keys that a query token sees.
-static Kv8Plan kv8_plan(const dkv_kv8_shape& sh, int num_seqs, int max_q, int span) {
+static Kv8Kind kv8_kind(const dkv_kv8_shape& sh, int max_q) {
   const int64_t rows = static_cast<int64_t>(max_q) * (sh.num_q_heads / sh.num_kv_heads);
-  Kv8Plan p;
-  const bool tiles = sh.dtype != DKV_F32 && rows > kStreamMaxRows;
-  p.tile = sh.dtype == DKV_F32 ? kSimpleRows : tiles ? kTileRows : rows <= 8 ? 8 : 16;
-  const int per_sm = sh.dtype == DKV_F32 ? 4 : tiles ? 1 : sh.head_dim == 64 ? stream_ctas<64>(p.tile / 8) : stream_ctas<128>(p.tile / 8);
-  const int64_t base = ceil_div64(rows, p.tile) * sh.num_kv_heads * std::max(num_seqs, 1);
-  const int64_t cells = ceil_div64(span, kKv8CellKeys);
-  const int64_t sms = tiles ? num_sms() / 2 : num_sms();  // the tcgen05 kernel's CTAs come in pairs
-  const int most = static_cast<int>(std::max<int64_t>(
-      1, std::min<int64_t>(kKv8MaxSplits, ceil_div64(cells, kKv8MinSplitCells))));
-  // Time in cells of one SM: the fullest SM's share of the cells, a start and an end for each of its rounds of CTAs, and
-  // with splits the join (tcgen05 kernel: 256 rows of fp32 written and read again per CTA).
-  p.nsplit = 1;
-  double best = 0;
-  for (int n = 1; n <= most; ++n) {
-    const int64_t ctas = base * n;
-    // (a CTA alone on its SM waits for its own latencies and is hardly faster than two that share one)
-    double t = static_cast<double>(std::max<int64_t>(ceil_div64(ctas, sms), std::min(per_sm, 2))) *
-                   (static_cast<double>(cells) / n) +
-               24.0 * static_cast<double>(ceil_div64(ctas, sms * per_sm));
-    if (n > 1) t += 20.0 + (tiles ? 40.0 * static_cast<double>(ceil_div64(ctas, sms)) : 0.0);
-    if (n == 1 || t < best) best = t, p.nsplit = n;
-  }
-  return p;
+  Kv8Kind k;
+  k.tiles = sh.dtype != DKV_F32 && rows > kStreamMaxRows;
+  k.tile = sh.dtype == DKV_F32 ? kSimpleRows : k.tiles ? kTileRows : rows <= 8 ? 8 : 16;
+  k.per_sm = sh.dtype == DKV_F32 ? 4 : k.tiles ? 1 : sh.head_dim == 64 ? stream_ctas<64>(k.tile / 8) : stream_ctas<128>(k.tile / 8);
+  k.slots = k.tiles ? num_sms() / 2 : num_sms();  // the tcgen05 kernel's CTAs come in pairs
+  k.most = (k.tiles ? 12 : 16) * k.slots * k.per_sm;
+  return k;
 }
 
-int kv8_attn_splits(const dkv_kv8_shape& sh, int num_seqs, int max_q, int max_ctx) {
-  return kv8_plan(sh, num_seqs, max_q, max_ctx).nsplit;
+// Most key ranges that a row of up to `span` keys is cut into.
+static int kv8_most_splits(int span) {
+  const int64_t cells = ceil_div64(span, kKv8CellKeys);
+  return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kKv8MaxSplits, ceil_div64(cells, kKv8MinSplitCells))));
+}
+
+// Key ranges that a row is cut into.  span: most keys that a query token sees.
+int kv8_attn_splits(const dkv_kv8_shape& sh, int num_seqs, int max_q, int span) {
+  const Kv8Kind k = kv8_kind(sh, max_q);
+  const int64_t rows = static_cast<int64_t>(max_q) * (sh.num_q_heads / sh.num_kv_heads);
+  const int64_t base = ceil_div64(rows, k.tile) * sh.num_kv_heads * std::max(num_seqs, 1);
+  const int64_t cells = ceil_div64(span, kKv8CellKeys);
+  const int most = kv8_most_splits(span);
+  // Time in cells of one SM: the fullest SM's share of the cells, a start and an end for each of its rounds of CTAs, and
+  // with splits the join (tcgen05 kernel: 256 rows of fp32 written and read again per CTA).
+  int nsplit = 1;
+  double best = 0;
+  for (int n = 1; n <= most && (n == 1 || n * base <= k.most); ++n) {
+    const int64_t ctas = base * n;
+    // (a CTA alone on its SM waits for its own latencies and is hardly faster than two that share one)
+    double t = static_cast<double>(std::max<int64_t>(ceil_div64(ctas, k.slots), std::min(k.per_sm, 2))) *
+                   (static_cast<double>(cells) / n) +
+               24.0 * static_cast<double>(ceil_div64(ctas, k.slots * k.per_sm));
+    if (n > 1) t += 20.0 + (k.tiles ? 40.0 * static_cast<double>(ceil_div64(ctas, k.slots)) : 0.0);
+    if (n == 1 || t < best) best = t, nsplit = n;
+  }
+  return nsplit;
+}
+
+// Query rows times splits that no call within these bounds exceeds.  The splits of a call go up and down with its batch, so
+// this is not the plan's own number but one that grows with every bound: a workspace for a program's largest step serves
+// its smaller ones.  (A call stages splits x total_q x H_q rows; they fill at most its CTAs' tiles.)
+int64_t kv8_attn_staged(const dkv_kv8_shape& sh, int64_t total_q, int max_q, int max_ctx) {
+  const int splits = kv8_most_splits(max_ctx);
+  if (splits == 1) return 0;
+  const Kv8Kind k = kv8_kind(sh, max_q);
+  return std::min<int64_t>(splits * total_q * sh.num_q_heads, k.most * k.tile);
 }
 
 // Joins the splits of each row; starts while the attention kernel's last CTAs run.  With more than 8 splits four warps share
@@ -119,7 +142,7 @@ static dkv_status attn_simple(const Kv8Attn& p, cudaStream_t st) {
   return launch_combine<T, D>(p, st);
 }
 
-dkv_status launch_kv8_attention(const Kv8AttnArgs& a, const Kv8AttnWs& w, void* workspace, cudaStream_t st) {
+dkv_status launch_kv8_attention(const Kv8AttnArgs& a, int nsplit, const Kv8AttnWs& w, void* workspace, cudaStream_t st) {
   const dkv_kv8_shape& sh = *a.shape;
   Kv8Attn p = {};
   p.codes = static_cast<const uint8_t*>(a.cache->codes);
@@ -135,10 +158,10 @@ dkv_status launch_kv8_attention(const Kv8AttnArgs& a, const Kv8AttnWs& w, void* 
     p.softcap = a.score->softcap, p.window = a.score->window < a.max_ctx ? a.score->window : 0, p.slopes = a.score->alibi_slopes;
     p.prefix_lens = a.score->prefix_lens, p.first_key = a.score->first_key;
   }
-  p.out = a.out, p.lse = a.lse, p.nsplit = w.nsplit;
-  if (p.window > 0)  // fewer keys to share out than the workspace was sized for
-    p.nsplit = std::min(p.nsplit, kv8_plan(sh, a.num_seqs, a.max_q, static_cast<int>(std::min<int64_t>(
-                                               a.max_ctx, int64_t{a.max_q} + p.window))).nsplit);
+  p.out = a.out, p.lse = a.lse, p.nsplit = nsplit;
+  if (p.window > 0)  // fewer keys to share out
+    p.nsplit = std::min(p.nsplit, kv8_attn_splits(sh, a.num_seqs, a.max_q, static_cast<int>(std::min<int64_t>(
+                                               a.max_ctx, int64_t{a.max_q} + p.window))));
   p.ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(workspace) + w.ml);
   p.o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.o);
   const bool e4 = sh.code == DKV_KV8_E4M3, d64 = sh.head_dim == 64;

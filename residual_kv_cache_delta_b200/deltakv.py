@@ -454,6 +454,7 @@ def kv8_cache_bytes(shape: KV8Shape, num_blocks: int) -> tuple[int, int]:
 
 
 def kv8_attention_workspace(shape: KV8Shape, num_seqs: int, total_q: int, max_q: int, max_ctx: int) -> int:
+    """Bytes of workspace for every call within these bounds (the size never falls as a bound grows)."""
     n = ctypes.c_size_t()
     _check(load_library().deltakv_kv8_attention_workspace(ctypes.byref(shape.c), num_seqs, total_q, max_q, max_ctx,
                                                           ctypes.byref(n)), "deltakv_kv8_attention_workspace")

@@ -703,3 +703,29 @@ def test_append_leaves_the_queries_of_refused_sequences(dtype):
                 else:
                     want = K.rotate(q[rows], rope[start[s]:start[s] + cu[s + 1] - cu[s]], False).to(dtype)
                 assert torch.equal(got[rows], want), (cu, start, inplace, s)
+
+
+@pytest.mark.parametrize("dtype,d", [(BF, 128), (BF, 64), (F32, 64)])
+def test_one_workspace_serves_every_step_of_a_program(dtype, d):
+    """A workspace sized once, for the largest batch, step and context: decode steps of batches that come and go, verification
+    and prefill chunks all run in it, and nothing behind its end is written."""
+    shape, T, most = D.KV8Shape(4, 2, d, 16, dtype, "int8"), 4000, 40
+    g = _gen(59)
+    ctx = [T - 61 * i for i in range(most)]
+    codes, scales, table = K.cache_for(shape, ctx, g)
+    cache, tab = D.KV8Cache(codes.cuda(), scales.cuda()), table.cuda()
+    need = D.kv8_attention_workspace(shape, most, 300, 200, T)
+    ws = torch.full((need + 4096,), 0xa5, dtype=torch.uint8, device="cuda")
+    for sizes in ([1], [1] * 2, [1] * 9, [1] * 18, [1] * 19, [1] * 37, [1] * 40, [5] * 3, [9, 1, 9], [20], [40, 3], [200, 100], [200]):
+        S, n, cu = len(sizes), sum(sizes), _cu(sizes)
+        q = torch.randn(n, 4, d, generator=g).to(dtype)
+        out = torch.full((n, 4, d), math.nan, dtype=dtype, device="cuda")
+        lse = torch.full((n, 4), math.nan, device="cuda")
+        D.deltakv_kv8_attention(shape, cache, q.cuda(), _i32(cu), _i32(ctx[:S]), tab[:S], max(sizes), T, out, lse, ws[:need])
+        rows = [i for i in range(S) if i in (0, S // 2, S - 1)]
+        for s in rows:  # a sequence at a time in fp64
+            part = slice(cu[s], cu[s + 1])
+            ro, rl, to, tl = K.attention(shape, codes, scales, table[s:s + 1], q[part], [0, sizes[s]], ctx[s:s + 1])
+            K.check(out[part], ro, to, "out")
+            K.check(lse[part], rl, tl, "lse")
+    assert (ws[need:] == 0xa5).all()

@@ -170,3 +170,22 @@ def test_append_refuses_tokens_without_room_for_them(lib):
         assert attend(lib, **bad) == ARG, bad
     for nothing in (dict(total=0, max_new=0, seqs=0), dict(total=0), dict(total=0, k=0, v=0, cu=0)):
         assert append(lib, **nothing) == OK, nothing
+
+
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+@pytest.mark.parametrize("hq,hkv,d", [(32, 8, 128), (8, 8, 64), (64, 8, 128), (16, 1, 64)])
+def test_a_workspace_for_the_largest_step_serves_every_smaller_one(lib, dtype, hq, hkv, d):
+    """The size never falls as a bound grows, whatever the split plan makes of the batch."""
+    sh = D.KV8Shape(hq, hkv, d, 16, dtype, "int8")
+    seqs, most_q, ctxs = (1, 2, 5, 37, 48, 74, 80, 128), (1, 2, 5, 16, 17, 64, 300, 2048), (16, 300, 4096, 32768, 131072)
+    need = {(s, q, t): D.kv8_attention_workspace(sh, s, s * q, q, t) for s in seqs for q in most_q for t in ctxs}
+    for axis, steps in enumerate((seqs, most_q, ctxs)):
+        for key, n in need.items():
+            i = steps.index(key[axis])
+            if i:
+                below = list(key)
+                below[axis] = steps[i - 1]
+                assert need[tuple(below)] <= n, (key, axis)
+    # fewer query rows than the bounds allow, and a bound that no longer grows with the batch
+    assert D.kv8_attention_workspace(sh, 8, 8, 300, 4096) <= need[37, 300, 4096]
+    assert max(need.values()) <= 512 << 20
