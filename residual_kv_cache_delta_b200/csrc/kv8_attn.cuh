@@ -7,17 +7,22 @@
 namespace dkv {
 
 // Up to so many rows per kv head the streaming kernel is taken (in row tiles of 16), above it the tcgen05 one, whose time
-// hardly depends on the rows below its tile.  Microseconds of the first and the second, 8 kv heads, int8:
-//                      16 rows         32 rows         64 rows
-//   d 128,  8 x  5000   30.5 and  94.8  48.7 and  94.9  94.6 and  96.7
-//           8 x 32768    153 and   541   281 and   537   510 and   539
-//           1 x  2000   11.5 and  16.5  11.7 and  16.8  13.9 and  17.8
-//   d  64,  8 x  5000   22.9 and  78.5  34.2 and  78.4  56.2 and  80.3
-//           8 x 32768   90.7 and   453   169 and   452   307 and   453
-//           1 x  2000   10.9 and  15.0  11.2 and  15.8  13.3 and  16.2
-// (The second figures are of builds with a lower limit, whose code is laid out differently: some per cent either way.)
-// At d = 128 the two are close at 64 rows.  At d = 64 the streaming kernel still leads there; more rows were not measured.
-constexpr int kStreamMaxRows = 64;
+// hardly depends on the rows below its tile.  Microseconds of the first and the second, both from one build, which takes either
+// by a switch; 8 kv heads, int8:
+//                      16 rows         32 rows         64 rows         80 rows         96 rows         128 rows
+//   d 128,  8 x  5000   30.9 and  94.4  49.6 and  95.6  95.2 and  97.8   139 and  98.3   141 and  97.6   188 and  99.3
+//           8 x 32768    153 and   534   283 and   536   511 and   538   662 and   539   779 and   541   980 and   542
+//           1 x  2000   12.0 and  16.9  12.3 and  17.2  14.5 and  18.4  16.0 and  18.9  16.4 and  19.9  18.1 and  20.5
+//           1 x 32768   26.9 and  73.6  40.5 and  73.8  76.1 and  75.1  95.7 and  75.7  99.6 and  76.5   144 and  77.7
+//   d  64,  8 x  5000   23.4 and  78.7  35.2 and  78.8  57.1 and  80.9  84.4 and  80.9  90.7 and  80.9   112 and  81.2
+//           8 x 32768   91.0 and   452   169 and   452   308 and   453   383 and   453   449 and   453   589 and   454
+//           1 x  2000   11.1 and  15.9  11.6 and  16.4  13.5 and  16.7  15.2 and  16.8  15.2 and  17.7  15.9 and  17.8
+//           1 x 32768   22.9 and  62.0  30.4 and  62.4  46.7 and  63.3  64.3 and  63.4  65.2 and  63.6  86.2 and  64.0
+// e4m3 takes up to 10% less in the first column and 3% in the second.  With one kv head, where neither fills the GPU, the first
+// leads further (d 128, 8 x 5000, 64 rows: 20.5 and 25.8; d 64, 80 rows: 19.8 and 23.3).  Capped scores take the second longer
+// (8 x 32768: 589 and 896 at 64 rows of d 128, 463 and 802 at 80 of d 64).
+template <int D>
+constexpr int kStreamMaxRows = D == 64 ? 80 : 64;
 
 // The kernel of a call: how many query rows a CTA (tcgen05: a pair) takes, how many of them an SM holds, and the most CTAs
 // that a call with splits may have.  That limit bounds the workspace (most x tile staged rows).  It is 16 rounds of CTAs (12
@@ -32,7 +37,7 @@ struct Kv8Kind {
 static Kv8Kind kv8_kind(const dkv_kv8_shape& sh, int max_q) {
   const int64_t rows = static_cast<int64_t>(max_q) * (sh.num_q_heads / sh.num_kv_heads);
   Kv8Kind k;
-  k.tiles = sh.dtype != DKV_F32 && rows > kStreamMaxRows;
+  k.tiles = sh.dtype != DKV_F32 && rows > (sh.head_dim == 64 ? kStreamMaxRows<64> : kStreamMaxRows<128>);
   k.tile = sh.dtype == DKV_F32 ? kSimpleRows : k.tiles ? kTileRows : rows <= 8 ? 8 : 16;
   k.per_sm = sh.dtype == DKV_F32 ? 4 : k.tiles ? 1 : sh.head_dim == 64 ? stream_ctas<64>(k.tile / 8) : stream_ctas<128>(k.tile / 8);
   k.slots = k.tiles ? num_sms() / 2 : num_sms();  // the tcgen05 kernel's CTAs come in pairs
@@ -123,7 +128,7 @@ template <int D, bool E4M3, bool BIAS>
 static dkv_status attn_rows(const Kv8Attn& p, cudaStream_t st) {
   const int64_t rows = static_cast<int64_t>(p.max_q) * p.group;
   if (rows <= 8) return attn_stream<D, E4M3, 1, BIAS>(p, st);
-  if (rows <= kStreamMaxRows) return attn_stream<D, E4M3, 2, BIAS>(p, st);
+  if (rows <= kStreamMaxRows<D>) return attn_stream<D, E4M3, 2, BIAS>(p, st);
   return attn_tile<D, E4M3, BIAS>(p, st);
 }
 

@@ -729,3 +729,12 @@ def test_one_workspace_serves_every_step_of_a_program(dtype, d):
             K.check(out[part], ro, to, "out")
             K.check(lse[part], rl, tl, "lse")
     assert (ws[need:] == 0xa5).all()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("mods", [(), ("softcap", "alibi", "window300", "prefix5")])
+def test_row_counts_on_either_side_of_a_kernel_s_limit(d, mods):
+    """Rows per kv head around 8, 16, 64, 80 and 96, where one kernel or row tile gives way to the next."""
+    shape = D.KV8Shape(2, 1, d, 16, BF, "e4m3")
+    for nq in (3, 4, 5, 8, 9, 31, 32, 33, 39, 40, 41, 47, 48, 49):
+        _attention_case(shape, [nq, 1], [700, 90], nq, mods)
