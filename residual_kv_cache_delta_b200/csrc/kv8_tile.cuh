@@ -26,6 +26,7 @@
 // maximum is raised (and O rescaled in tensor memory) only when a row passes it by more than 2^8.
 #pragma once
 
+#include <algorithm>
 #include <cstddef>
 
 #include "kv8_append.cuh"
@@ -46,12 +47,13 @@ struct __align__(16) TileMeta {  // of one key tile
   int there, last, pad[2];  // cells that are mapped; the last key, INT_MAX where the cells are not mapped keys in a row
 };
 
-// Bytes of a CTA's shared memory: 256 rows of Q, its halves of K and V as fp16.
+// Bytes of a CTA's shared memory: 256 rows of Q, its halves of K and V as fp16.  At least more than half of an SM's: a CTA takes
+// all of its SM's tensor memory, and two pairs that share two SMs and each get one of them would wait for one another.
 template <int D>
 struct TileSmem {
   static constexpr uint32_t kQ = 128 * D * 2, kHalf = kTileKeys * D;
   static constexpr uint32_t q = 0, k = q + 2 * kQ, v = k + kTileStages * kHalf, total = v + kTileStages * kHalf;
-  static constexpr size_t bytes = 1024 + total;
+  static constexpr size_t bytes = std::max<size_t>(1024 + total, 116 * 1024);
 };
 
 struct TileBars {

@@ -738,3 +738,37 @@ def test_row_counts_on_either_side_of_a_kernel_s_limit(d, mods):
     shape = D.KV8Shape(2, 1, d, 16, BF, "e4m3")
     for nq in (3, 4, 5, 8, 9, 31, 32, 33, 39, 40, 41, 47, 48, 49):
         _attention_case(shape, [nq, 1], [700, 90], nq, mods)
+
+
+def test_prefills_and_compress_on_streams_of_their_own():
+    """Kernels that take a whole SM's tensor memory, launched side by side: many-row attention with both head sizes on two
+    streams, the compressed cache's search on a third.  Each ends, and with the bits of a run by itself."""
+    g = _gen(61)
+    w = synth.workload(1, seq_len=1500, num_kv_heads=2, num_q_heads=8)
+    L = C.make_layer(w, [1500, 900])
+    alone = C.gpu_compress(L)
+    runs = []
+    for d, code, cap in ((64, "int8", 0.0), (64, "e4m3", 30.0), (128, "int8", 0.0)):
+        shape, T = D.KV8Shape(8, 2, d, 16, BF, code), 1800
+        codes, scales, table = K.cache_for(shape, [T], g)
+        cache = D.KV8Cache(codes.view(torch.uint8).cuda().view(shape.code_dtype), scales.cuda())
+        q = torch.randn(T, 8, d, generator=g).to(BF).cuda()
+        args = (shape, cache, q, _i32([0, T]), _i32([T]), table.cuda(), T, T)
+        bufs = [(torch.empty_like(q), torch.empty(T, 8, device="cuda"),
+                 D.alloc_workspace(D.kv8_attention_workspace(shape, 1, T, T, T))) for _ in range(2)]
+        D.deltakv_kv8_attention(*args, *bufs[0], softcap=cap)
+        runs.append((args, cap, bufs, torch.cuda.Stream()))
+    side = torch.cuda.Stream()
+    cache2 = D.alloc_cache(C.shape_of(w), L.num_blocks, "cuda")
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for args, cap, bufs, st in runs:
+            for _ in range(3):
+                D.deltakv_kv8_attention(*args, *bufs[1], softcap=cap, stream=st)
+        with torch.cuda.stream(side):
+            C.gpu_compress(L, cache=cache2)
+    torch.cuda.synchronize()
+    assert D.deltakv_get_device_error() == 0
+    for args, cap, bufs, st in runs:
+        assert torch.equal(bufs[0][0], bufs[1][0]) and torch.equal(bufs[0][1], bufs[1][1])
+    assert torch.equal(alone.codes, cache2.codes) and torch.equal(alone.ref_idx, cache2.ref_idx)
