@@ -332,6 +332,9 @@ dkv_status deltakv_decode_attention_noalloc(const dkv_shape* shape, const dkv_pa
  * scale, and when it grows the earlier rows' codes become sat(RNE(code * (s_old * (1 / s_h)))).  A scale never
  * shrinks while its block is filled.  A value that is not finite sets the scale to NaN and its call's codes to 0: every
  * value of that block, head and half then reads as NaN until an append writes the block from its first row again.
+ * Attention gives NaN in out to the query heads that see such a block, and in lse where its K is NaN (where its V is, lse may
+ * be NaN or finite); rows that do not see it are as without it.  Codes are finite: append writes no e4m3 NaN (0x7f, 0xff),
+ * and at positions below a context's length there must be none, seen or not.  Behind the length any byte may stand.
  * ------------------------------------------------------------------------------------------------------------ */
 typedef enum dkv_kv8_code { DKV_KV8_INT8 = 0, DKV_KV8_E4M3 = 1 } dkv_kv8_code;
 

@@ -1,10 +1,10 @@
 // Append to the 8-bit paged cache: position rotation of K (and q), quantisation, paged write.
 //
 // Bound by memory: every input value is read once and every code written once (two prompts of 32768 tokens, 32 + 2 x 8 heads
-// of 128: 212 us, 5.8 TB/s with 80 registers; an earlier build took 216 us with 72, 235 with 64 and 233 with 98).
-// A CTA owns K or V of one block of one
-// sequence for a few kv heads; a thread owns 16 dimensions of one row ("unit"), so that a block's largest magnitude is a
-// reduction over registers, and loads several heads at once, before anything that it does not need for their addresses.
+// of 128: 211 us, 5.8 TB/s with 80 registers; an earlier build took 216 us with 72, 235 with 64 and 233 with 98).
+// A CTA owns K or V of one block of one sequence for a few kv heads; a thread owns 16 dimensions of one row ("unit"), so that a
+// block's largest magnitude is a reduction over registers, and loads several heads at once, before anything that it does not
+// need for their addresses.
 // Unit u of a rotated row holds dimensions whose partners it also holds: 8u .. 8u+7 of the first half and of the second
 // (halves), or 16u .. 16u+15 (pairs); both use entries 8u .. 8u+7 of the cosines and sines, which stay in registers.
 #pragma once

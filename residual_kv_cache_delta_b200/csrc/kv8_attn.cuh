@@ -137,14 +137,14 @@ static dkv_status attn_bf16(const Kv8Attn& p, cudaStream_t st) {
   return p.softcap > 0.f || p.slopes ? attn_rows<D, E4M3, true>(p, st) : attn_rows<D, E4M3, false>(p, st);
 }
 
-template <typename T, int D, bool E4M3>
+template <int D, bool E4M3>
 static dkv_status attn_simple(const Kv8Attn& p, cudaStream_t st) {
   const int row_tiles = static_cast<int>(ceil_div64(static_cast<int64_t>(p.max_q) * p.group, kSimpleRows));
   const int64_t ctas = static_cast<int64_t>(p.nsplit) * row_tiles * p.heads * p.num_seqs;
   if (ctas > INT32_MAX) return DKV_ERR_UNSUPPORTED;
-  kv8_attn_simple_kernel<T, D, E4M3><<<static_cast<unsigned>(ctas), 128, 0, st>>>(p, row_tiles);
+  kv8_attn_simple_kernel<D, E4M3><<<static_cast<unsigned>(ctas), 128, 0, st>>>(p, row_tiles);
   if (cudaGetLastError() != cudaSuccess) return DKV_ERR_CUDA;
-  return launch_combine<T, D>(p, st);
+  return launch_combine<float, D>(p, st);
 }
 
 dkv_status launch_kv8_attention(const Kv8AttnArgs& a, int nsplit, const Kv8AttnWs& w, void* workspace, cudaStream_t st) {
@@ -171,8 +171,8 @@ dkv_status launch_kv8_attention(const Kv8AttnArgs& a, int nsplit, const Kv8AttnW
   p.o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + w.o);
   const bool e4 = sh.code == DKV_KV8_E4M3, d64 = sh.head_dim == 64;
   if (sh.dtype == DKV_F32) {
-    if (d64) return e4 ? attn_simple<float, 64, true>(p, st) : attn_simple<float, 64, false>(p, st);
-    return e4 ? attn_simple<float, 128, true>(p, st) : attn_simple<float, 128, false>(p, st);
+    if (d64) return e4 ? attn_simple<64, true>(p, st) : attn_simple<64, false>(p, st);
+    return e4 ? attn_simple<128, true>(p, st) : attn_simple<128, false>(p, st);
   }
   if (d64) return e4 ? attn_bf16<64, true>(p, st) : attn_bf16<64, false>(p, st);
   return e4 ? attn_bf16<128, true>(p, st) : attn_bf16<128, false>(p, st);

@@ -14,7 +14,7 @@ namespace dkv {
 
 constexpr int kSimpleRows = 8, kSimpleKeys = 32;
 
-template <typename T, int D, bool E4M3>
+template <int D, bool E4M3>
 __global__ void __launch_bounds__(128) kv8_attn_simple_kernel(const Kv8Attn a, int row_tiles) {
   constexpr int kPad = D + 4;
   __shared__ __align__(16) float sk[kSimpleKeys * kPad];
@@ -49,8 +49,7 @@ __global__ void __launch_bounds__(128) kv8_attn_simple_kernel(const Kv8Attn a, i
     const int r = r0 + e / D;
     float x = 0.f;
     if (r < r1)
-      x = Elem<T>::to_f(static_cast<const T*>(
-          a.q)[(sq_.q0 + r / a.group) * a.q_stride + (h * a.group + r % a.group) * D + e % D]);
+      x = static_cast<const float*>(a.q)[(sq_.q0 + r / a.group) * a.q_stride + (h * a.group + r % a.group) * D + e % D];
     sq[e] = x * a.scale;
   }
   float m[2] = {kNoMax, kNoMax}, l[2] = {0.f, 0.f}, acc[kSimpleRows] = {};
@@ -154,7 +153,7 @@ __global__ void __launch_bounds__(128) kv8_attn_simple_kernel(const Kv8Attn a, i
       if (tid == 0) a.ml[prow] = make_float2(mm, ll);
       if (tid < D && ll != 0.f) a.o[prow * D + tid] = o;
     } else {
-      if (tid < D) static_cast<T*>(a.out)[at * D + tid] = Elem<T>::from_f(ll == 0.f ? 0.f : o / ll);
+      if (tid < D) static_cast<float*>(a.out)[at * D + tid] = ll == 0.f ? 0.f : o / ll;
       if (tid == 0 && a.lse) a.lse[at] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * kLn2;
     }
   }

@@ -3,8 +3,10 @@
 //
 // A row is a query token and a head of the kv head's group; a CTA takes 8 NT rows and a range of keys, its warps take
 // the range's 16-key cells in turn.  Bound by memory at 8 rows: 8 x 32768 tokens, 8 kv heads, d = 128 take 96 us (5.6 TB/s,
-// 86% of the measured copy rate; issue slots 58% busy).  Each warp has its own ring of cells in shared memory (two tensor-map boxes of 16
-// rows, K and V) and waits for nobody else, so there is no CTA barrier until the warps' results are joined.
+// 86% of the measured copy rate; issue slots 58% busy).  More than 16 rows are several CTAs, each of which reads, converts and
+// multiplies the whole cache again: 17 to 80 rows take time in proportion (64 rows there: 511 us), bound by issue and not memory.
+// Each warp has its own ring of cells in shared memory (two tensor-map boxes of 16 rows, K and V) and waits for nobody else,
+// so there is no CTA barrier until the warps' results are joined.
 //
 //   scores   S[16 keys][8 rows] = K q^T: the keys are the MMA's 16 rows, the query rows its 8 columns, so that no
 //            part of the MMA is padding for 8 rows.  A lane reads 16 or 32 bytes of two keys; the dimensions are
@@ -16,7 +18,8 @@
 // to 2^-24 of the row's largest value.  The cell's K scale multiplies the fp32 score.  Its V scale goes into the
 // exponent: with z = score + log2(v scale), the weights 2^(z - max z) are what multiplies V's codes, at most 2^4 and so
 // in fp16's range with 11 bits whatever the scales are, and the softmax sum adds 2^(z - max z) / (v scale) in fp32.
-// The running maximum is raised only when a score passes it by more than 2^4 (a warp vote per cell).
+// The running maximum is raised only when a score passes it by more than 2^4 (a warp vote per cell).  exp2 and log2 are the
+// hardware's (2^-21 of the weight).
 //
 // Key order inside a cell: MMA row g stands for key kPerm[g] (and 8 + kPerm[g]), chosen so that with the tensor map's
 // swizzle neither the K reads (16 bytes, lanes of two keys) nor the V reads (lanes of four keys) conflict on banks.

@@ -772,3 +772,21 @@ def test_prefills_and_compress_on_streams_of_their_own():
     for args, cap, bufs, st in runs:
         assert torch.equal(bufs[0][0], bufs[1][0]) and torch.equal(bufs[0][1], bufs[1][1])
     assert torch.equal(alone.codes, cache2.codes) and torch.equal(alone.ref_idx, cache2.ref_idx)
+
+
+@pytest.mark.parametrize("nq", [1, 4, 100])
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_sequences_that_share_blocks(dtype, nq):
+    """Sequences with one prefix in the same physical blocks, one of them there twice."""
+    shape = D.KV8Shape(6, 2, 64, 16, dtype, "e4m3")
+    g = _gen(67)
+    ctx = [300, 208 + nq, 300, 300]
+    codes, scales, table = K.cache_for(shape, ctx, g)
+    table[1, :13] = table[0, :13]
+    table[2] = table[0]
+    q = torch.randn(4 * nq, 6, 64, generator=g).to(dtype)
+    cu = _cu([nq] * 4)
+    out, lse = K.run_attention(shape, codes, scales, table, q, cu, ctx, "cuda")
+    ro, rl, to, tl = K.attention(shape, codes, scales, table, q, cu, ctx)
+    K.check(lse, rl, tl, "lse")
+    K.check(out, ro, to, "out")
