@@ -1,5 +1,6 @@
 // Attention over the 8-bit cache on CUDA cores, fp32 arithmetic throughout: the path of fp32 tensors.  8 x 32768 tokens of
-// d = 128, 4 heads per kv head took it 864 us with bf16 tensors, 0.6 TB/s: memory does not bound it.
+// d = 128, 8 kv heads, 4 heads each: 818 us, 0.66 TB/s, where memory alone would take 82; 512 tokens at 8192 keys: 5.8 ms.
+// Bound by its scalar products and three CTA barriers per 32 keys.
 //
 // One CTA takes kRows query rows (a row is a query token and a head of the kv head's group) and a range of keys.
 // Tiles of 32 keys are dequantised into shared memory; a warp scores two rows against the tile (one key per lane),

@@ -4,7 +4,8 @@
 // A row is a query token and a head of the kv head's group; a CTA takes 8 NT rows and a range of keys, its warps take
 // the range's 16-key cells in turn.  Bound by memory at 8 rows: 8 x 32768 tokens, 8 kv heads, d = 128 take 96 us (5.6 TB/s,
 // 86% of the measured copy rate; issue slots 58% busy).  More than 16 rows are several CTAs, each of which reads, converts and
-// multiplies the whole cache again: 17 to 80 rows take time in proportion (64 rows there: 511 us), bound by issue and not memory.
+// multiplies the whole cache again: 17 to 80 rows take time in proportion (32 and 64 rows there: 282 and 510 us), and what
+// bounds them is the latency of the 8 warps that an SM holds (32 rows: issue slots 41% busy, tensor pipe 22%, DRAM 24%).
 // Each warp has its own ring of cells in shared memory (two tensor-map boxes of 16 rows, K and V) and waits for nobody else,
 // so there is no CTA barrier until the warps' results are joined.
 //
